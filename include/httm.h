@@ -422,6 +422,220 @@ httm_status httm_profile_read(httm_plan_t plan, float* ms, int32_t* launches);
 httm_status httm_select_outliers_noalloc(const float* dev, const uint8_t* eligible, int32_t h, int32_t N,
                                          int32_t outlier_pct, uint8_t* mask, int32_t* n_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the layer.  A VGGT-style block normalises the token
+ * stream, projects it to heads, turns queries and keys by their positions,
+ * attends, projects back, and adds the gated result to the stream before
+ * the next norm.  The entry points below are that block's operators other
+ * than its library matrix products, with their gradients: they need no plan
+ * and work beside httm_forward (whose [h, N, d] tensors httm_rotary writes
+ * directly).  They are asynchronous on `stream`, run on the current device,
+ * allocate nothing, and are bit-deterministic for identical inputs (no
+ * atomics on results).  Calls may overlap on the GPU, from any threads, as
+ * long as they share neither outputs nor workspaces.  The conventions at the
+ * head of this file hold, with one difference: there is no status word in a
+ * workspace; httm_ops_device_status() reads one per device.
+ * ---------------------------------------------------------------------- */
+
+/* A [batch, heads, tokens, d_head] tensor anywhere in device memory: strides
+ * in elements, channels contiguous.  The stride of an extent of 1 is
+ * ignored. */
+typedef struct {
+  void* data;
+  int64_t batch, head, token;
+} httm_view;
+
+/*
+ * Attention over key ranges.  Query i of batch entry b attends to the keys
+ * j with key_begin[b, i] <= j < key_end[b, i] (both clamped to [0, kv_len]):
+ *   out_i = sum_j P_ij V_j,  P_ij = exp(softmax_scale * q_i . k_j - lse_i).
+ * One pair of ranges covers full, causal, sliding-window, frame-causal,
+ * padded and packed (block-diagonal) attention.
+ *  batch, heads, kv_heads   heads is a multiple of kv_heads; query head n
+ *                    reads key head n / (heads / kv_heads).
+ *  q_len, kv_len     0 is allowed; q_len <= 2,097,152, kv_len <= 2^30.
+ *  d_head            8 to 64 in steps of 8 (the tiles are 64 wide: a
+ *                    narrower head costs as much as one of 64).
+ *  dtype             HTTM_BF16 (other types: HTTM_ERR_UNSUPPORTED).
+ *  softmax_scale     0 selects 1 / sqrt(d_head); negative or not finite:
+ *                    HTTM_ERR_ARG.
+ *  key_begin, key_end  DEVICE int32 [batch, q_len], or NULL: 0 / kv_len.
+ * A query whose range is empty has out = 0, lse = -infinity and takes no
+ * part in the gradients.  What lies outside every range is not read into
+ * any result: a key or value no query of its batch entry attends to, and a
+ * query, dout or out row whose range is empty, may hold anything (infinities
+ * and NaN too).  A non-finite value that some query does attend to may
+ * reach every query within 256 rows of that one, also those that do not see
+ * it, and so may a non-finite query or dout row in the gradients of the keys
+ * of its tiles.
+ * Strides are multiples of 8 elements and data pointers 16-byte aligned
+ * (else HTTM_ERR_ALIGN).  Inputs may be broadcast (stride 0 over batch or
+ * heads; their gradients are then those of every copy, for the caller to
+ * add up); outputs may not overlap themselves or an input.
+ */
+typedef struct {
+  int32_t batch, heads, kv_heads, q_len, kv_len, d_head;
+  int32_t dtype; /* httm_dtype */
+  float softmax_scale;
+  const int32_t* key_begin;
+  const int32_t* key_end;
+} httm_attention;
+
+/* Workspace bytes of the two calls (host only; either output may be NULL).
+ * The workspace is 256-byte aligned device memory; 0 bytes: NULL will do. */
+httm_status httm_attention_workspace_bytes(const httm_attention* a, size_t* forward, size_t* backward);
+
+/*
+ * httm_attention_forward: q, out [batch, heads, q_len, d_head]; k, v [batch,
+ * kv_heads, kv_len, d_head]; lse (optional) fp32 [batch, heads, q_len]
+ * contiguous, natural logarithm.  Serves prefill and single tokens alike:
+ * with few query rows the keys are split over the SMs and joined.
+ */
+httm_status httm_attention_forward(const httm_attention* a, const httm_view* q, const httm_view* k,
+                                   const httm_view* v, const httm_view* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * httm_attention_backward: the gradients dq, dk, dv of sum(dout * out), with
+ * out and lse as httm_attention_forward left them for the same q, k, v and
+ * ranges.  The probabilities are recomputed from q, k and lse.  dk and dv
+ * add up the query heads that share a key head.  lse itself has no gradient.
+ */
+httm_status httm_attention_backward(const httm_attention* a, const httm_view* dout, const httm_view* q,
+                                    const httm_view* k, const httm_view* v, const httm_view* out, const float* lse,
+                                    const httm_view* dq, const httm_view* dk, const httm_view* dv, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions.  The first 2 * axes * pairs channels of a head are cut
+ * in `axes` runs of 2 * pairs, one per position coordinate (VGGT turns one
+ * half of a head by the patch's row and the other by its column: axes = 2).
+ * Pair n of a run turns by the angle position * freqs[n]:
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin);
+ * the channels behind them are copied.  inverse != 0 turns the other way,
+ * which is the gradient's map (the turn is orthogonal up to `factor`).
+ *  layout            HTTM_ROTARY_HALF: pair n is channels (n, pairs + n) of
+ *                    its run; HTTM_ROTARY_PAIRS: (2n, 2n + 1).
+ *  batch, tokens     may be 0.
+ *  heads, kv_heads   heads of the two tensors turned in one launch;
+ *                    kv_heads = 0: no second tensor (k, k_out ignored).
+ *  d_head            1 to 1024; dtype HTTM_BF16 or HTTM_F32.
+ *  axes              1 to 4;  pairs >= 1.
+ *  positions         DEVICE int32 [batch, tokens, axes], entries of batch b
+ *                    at b * position_batch (0: shared); any sign.
+ *  freqs             DEVICE float64 [pairs], radians per position.  Angles
+ *                    are reduced exactly in 64-bit fixed point (turns), so
+ *                    far positions lose nothing.
+ * Every stride is free (channels contiguous); out may be the input itself
+ * (same data and strides), and may not overlap it otherwise.
+ */
+typedef enum { HTTM_ROTARY_HALF = 0, HTTM_ROTARY_PAIRS = 1 } httm_rotary_layout;
+
+typedef struct {
+  int32_t batch, tokens, heads, kv_heads, d_head;
+  int32_t dtype;  /* httm_dtype */
+  int32_t axes, pairs;
+  int32_t layout; /* httm_rotary_layout */
+  int32_t inverse;
+  float factor;
+  const int32_t* positions;
+  int64_t position_batch;
+  const double* freqs;
+} httm_rotary_cfg;
+
+httm_status httm_rotary(const httm_rotary_cfg* c, const httm_view* q, const httm_view* q_out, const httm_view* k,
+                        const httm_view* k_out, void* stream);
+
+/*
+ * The norms before and after a block, fused with its gate and residual.
+ *   y = residual_scale * x + gate * Post(f),   stored in stream_dtype;
+ *   z = Pre(y as stored),                      stored in branch_dtype.
+ * x is the token stream, f the block's output, y the new stream and z the
+ * next block's input.  Post and Pre are LayerNorm or RMSNorm over the
+ * channels, with their own weight, bias and eps, or absent.  Statistics and
+ * sums are fp32.
+ *  rows, channels    rows >= 0; channels 1 to 8192.
+ *  stream_dtype      of x, y, dy, dx;  branch_dtype: of f, z, dz, df:
+ *                    bf16/bf16, fp32/bf16 or fp32/fp32.
+ *  post, pre         httm_norm_kind.  HTTM_NORM_NONE for post: f itself;
+ *                    for pre: no z.
+ *  gates             0: no gate (1); g: gate is [g, channels], each row
+ *                    serving rows / g consecutive rows (rows must be a
+ *                    multiple of g; g <= 1024).  LayerScale has one.
+ * Weights are DEVICE fp32 arrays of `channels`; a NULL weight is 1, a NULL
+ * bias 0 (RMSNorm takes a bias too).
+ */
+typedef enum { HTTM_NORM_NONE = 0, HTTM_NORM_LAYER = 1, HTTM_NORM_RMS = 2 } httm_norm_kind;
+
+typedef struct {
+  int64_t rows;
+  int32_t channels;
+  int32_t stream_dtype, branch_dtype; /* httm_dtype */
+  int32_t post, pre;                  /* httm_norm_kind */
+  int32_t gates;
+  float post_eps, pre_eps;
+  float residual_scale;
+} httm_norm_cfg;
+
+/* [rows, channels], `row` elements from one row to the next (any value). */
+typedef struct {
+  void* data;
+  int64_t row;
+} httm_rows;
+
+typedef struct {
+  const float* gate;
+  const float* post_weight;
+  const float* post_bias;
+  const float* pre_weight;
+  const float* pre_bias;
+} httm_norm_weights;
+
+/* Gradient outputs, fp32, each optional. */
+typedef struct {
+  float* gate; /* [gates, channels] */
+  float* post_weight;
+  float* post_bias;
+  float* pre_weight;
+  float* pre_bias;
+} httm_norm_grads;
+
+/*
+ * httm_gated_norm_forward.  f NULL: no block output (post NONE and gates 0);
+ * then y may be NULL too if residual_scale is 1 (z = Pre(x)).  y may be x
+ * itself (same data and stride).  z is NULL exactly when pre is NONE.
+ * stats: fp32 [4, rows], written for the backward call (mean and 1 /
+ * deviation of f, then of y; unused rows are left as they are); NULL if no
+ * backward call follows.
+ */
+httm_status httm_gated_norm_forward(const httm_norm_cfg* c, const httm_norm_weights* w, const httm_rows* x,
+                                    const httm_rows* f, const httm_rows* y, const httm_rows* z, float* stats,
+                                    void* stream);
+
+/* Workspace bytes of httm_gated_norm_backward (host only). */
+httm_status httm_gated_norm_workspace_bytes(const httm_norm_cfg* c, size_t* bytes);
+
+/*
+ * httm_gated_norm_backward: the gradients of sum(dy * y) + sum(dz * z).  dy
+ * NULL: the stream's gradient is 0; dz is NULL exactly when pre is NONE.  f,
+ * y and stats as the forward call had and left them (f NULL as there; y may
+ * be NULL if pre is NONE; x stands in for y where the forward call had none).
+ * dx, df and every member of grads are optional; dx may be dy itself.
+ */
+httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_weights* w, const httm_rows* dy,
+                                     const httm_rows* dz, const httm_rows* f, const httm_rows* y, const float* stats,
+                                     const httm_rows* dx, const httm_rows* df, const httm_norm_grads* grads,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The operators' device status: synchronises `stream`, then reads the HTTM_DEV_*
+ * bits that their kernels set on the current device since the last call and
+ * clears them.  HTTM_DEV_TIMEOUT: a bounded wait (2 s) ran out; the outputs
+ * of the calls since then are undefined, the context stays usable.  Returns
+ * HTTM_ERR_TIMEOUT when bits were set.  Not during a stream capture.
+ */
+httm_status httm_ops_device_status(void* stream, uint32_t* status);
+
 const char* httm_status_str(httm_status s);
 
 /*

@@ -29,6 +29,9 @@ EXPORTS = (
     "httm_select_outliers_noalloc", "httm_set_wait_budget", "httm_status_str",
     "httm_plan_shard", "httm_forward_sharded", "httm_last_cuda_error", "httm_set_fused_unmerge",
     "httm_plan_partition",
+    "httm_attention_workspace_bytes", "httm_attention_forward", "httm_attention_backward", "httm_rotary",
+    "httm_gated_norm_forward", "httm_gated_norm_workspace_bytes", "httm_gated_norm_backward",
+    "httm_ops_device_status",
 )
 STAGES = ("match", "merge", "outlier", "attention", "unmerge", "other")
 
@@ -118,6 +121,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("httm_plan", "httm_get_plan_info", "httm_forward", "httm_forward_debug",
                  "httm_forward_with_plan", "httm_forward_reuse", "httm_reorder", "httm_get_device_status",
                  "httm_profile_enable", "httm_profile_read", "httm_plan_shard", "httm_forward_sharded"):
+        getattr(lib, name).restype = ctypes.c_int
+    # the operators around the layer: every argument is a pointer, or a size behind its workspace pointer
+    lib.httm_attention_workspace_bytes.argtypes = [P, P, P]
+    lib.httm_attention_forward.argtypes = [P] * 7 + [S, V]
+    lib.httm_attention_backward.argtypes = [P] * 11 + [S, V]
+    lib.httm_rotary.argtypes = [P] * 5 + [V]
+    lib.httm_gated_norm_forward.argtypes = [P] * 7 + [V]
+    lib.httm_gated_norm_workspace_bytes.argtypes = [P, P]
+    lib.httm_gated_norm_backward.argtypes = [P] * 11 + [S, V]
+    lib.httm_ops_device_status.argtypes = [V, ctypes.POINTER(U)]
+    for name in ("httm_attention_workspace_bytes", "httm_attention_forward", "httm_attention_backward", "httm_rotary",
+                 "httm_gated_norm_forward", "httm_gated_norm_workspace_bytes", "httm_gated_norm_backward",
+                 "httm_ops_device_status"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

@@ -99,6 +99,9 @@ namespace {
 thread_local cudaError_t t_last_err = cudaSuccess;
 thread_local const char* t_last_where = "";
 
+}  // namespace
+
+namespace httm {
 httm_status cuda_fail(cudaError_t e, const char* where) {
   t_last_err = e;
   t_last_where = where;
@@ -108,7 +111,7 @@ httm_status cuda_fail(cudaError_t e, const char* where) {
 // HTTM_SYNC_CHECK=1 in the environment: synchronise the stream after every
 // launch, so that a fault is attributed to the kernel that raised it (a
 // debugging aid; it serialises the forward).
-bool sync_check() {
+static bool sync_check() {
   static const bool on = [] {
     const char* v = getenv("HTTM_SYNC_CHECK");
     return v && v[0] == '1';
@@ -122,6 +125,10 @@ cudaError_t checked(cudaError_t e, cudaStream_t s) {
   const cudaError_t e2 = cudaDeviceSynchronize();    // every stream of the call (the key branch too)
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
+
+}  // namespace httm
+
+namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

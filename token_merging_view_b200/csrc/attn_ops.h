@@ -1,0 +1,62 @@
+// Attention over key ranges: what its kernels and their host side share.
+#pragma once
+#include <cuda.h>
+
+#include "ops.h"
+
+namespace httm {
+
+constexpr int kAttnTile = 128;          // keys, or query rows, of one tensor-core tile
+constexpr int kAttnD = 64;              // channels of a tile; narrower heads are padded with zeros
+constexpr int kAttnMaxQ = 1 << 21;      // queries of one sequence
+constexpr int kAttnMaxParts = 64;       // key splits of one forward work item
+
+// One call, passed to the kernels by value.
+struct AttnArgs {
+  int B, H, K, G, L, N, d;              // G = H / K query heads share a key head
+  float scale, scale_log2;              // softmax scale; times log2(e)
+  const int32_t *kb, *ke;               // [B, L], or null
+  View q, k, v, out, dout, dq, dk, dv;
+  const float* lse_in;
+  float* lse;
+  DevState* st;
+};
+
+// The 4-D tensor map (channels, tokens, heads, batch) of a bf16 view, boxes
+// of 128 tokens x 64 channels with 128-byte swizzle; what lies behind the
+// last token or channel reads as zero.  A broadcast dimension (stride 0) has
+// extent 1 in the map: its coordinate is multiplied by 0.  `spare`: the base
+// address where the view has none (no tokens: nothing is loaded through it).
+struct AttnMap {
+  CUtensorMap map;
+  int hmul, bmul;
+};
+bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch);
+
+// Forward: work items of up to 256 query rows, each in `parts` key ranges.
+struct AttnFwdPlan {
+  int rows, row_tiles, parts;           // rows = L * G of one key head
+  long long items;                      // B * K * row_tiles
+  size_t part_bytes;
+};
+AttnFwdPlan attn_fwd_plan(const httm_attention& a);
+cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s);
+
+// Backward workspace: per query row lse * log2(e) and D = dout . out, padded
+// to whole tiles, the key range of every query row and of every query tile,
+// then the partial sums of split key tiles.
+struct AttnTileRange {
+  int lo, hi;      // union of the live rows' ranges (lo >= hi: none)
+  int flo, fhi;    // intersection: keys [flo, fhi) are seen by every live row
+  int dead;        // rows of the sequence with an empty range
+  int pad[3];
+};
+struct AttnBwdPlan {
+  int q_tiles, k_tiles, Lp;             // Lp = q_tiles * 128
+  int kv_parts;                         // splits of the queries of one key tile
+  size_t stat, range, tiles, part, total;
+};
+AttnBwdPlan attn_bwd_plan(const httm_attention& a);
+cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, cudaStream_t s);
+
+}  // namespace httm

@@ -1,0 +1,733 @@
+// Attention over key ranges, backward.  With P_ij = exp(c q_i.k_j - lse_i)
+// recomputed from q, k and lse, and D_i = dout_i . out_i:
+//   dV = P^T dO,  dP = dO V^T,  dS = P o (dP - D),  dQ = c dS K,  dK = c dS^T Q.
+//
+// Three launches (a fourth when key tiles are split):
+//  - attn_prep_kernel: D and lse * log2(e) of every query row, padded to
+//    whole tiles (rows outside the sequence or with an empty range get
+//    lse = +inf, so their P is 0 without a compare), and the key ranges of
+//    rows and of query tiles;
+//  - attn_dkv_kernel: a CTA owns 128 keys and walks over the query tiles
+//    that see them, for all query heads sharing the key head; dK and dV stay
+//    in TMEM.  Everything is transposed (rows = keys): S^T = K Q^T and dP^T
+//    = V dO^T, so that P^T and dS^T are written back to TMEM as the A
+//    operands of dV += P^T dO and dK += dS^T Q, and nothing passes through
+//    shared memory but the loaded tiles;
+//  - attn_dq_kernel: a CTA owns 128 queries and walks over their keys; dS is
+//    the A operand of dQ += dS K.
+// Seven products a tile where one fused pass has five: dQ gathered from
+// key-owning CTAs needs either atomics, whose order would change the result
+// from run to run, or N x N / 128 partial sums.
+//
+// Both kernels: warp 0 loads (TMA), warp 1 issues tcgen05.mma, warps 4..11
+// compute -- all eight on the same tile, warpgroup w on its columns [64 w,
+// 64 w + 64), TMEM lane = row.  Products alternate S_0 dP_0 S_1 dP_1 ...
+// through a ring of three 128-column TMEM buffers; P or dS overwrites its
+// own warpgroup's columns of the product it came from (32 columns of bf16
+// pairs at 0 and at 64).  While dS_i is computed the tensor core does the
+// products that P_i freed, and the other way round.
+//
+// Parity waits: p_ready / s_read and ds_ready are two barriers each, used
+// by even and odd steps: step i + 2 cannot be reached by any warp before
+// the issuing warp has seen step i (its products are issued behind that
+// wait), so no barrier is ever two phases from a wait on it and none gets
+// an arrival of a later step early.
+#include <algorithm>
+
+#include "attn_ops.cuh"
+
+namespace httm {
+namespace {
+
+using namespace tc;
+
+constexpr int kStages = 4;
+constexpr int kThreads = 384;
+constexpr int kMaxQTiles = kAttnMaxQ / kAttnTile;
+constexpr uint32_t kColA = 384, kColB = 448;          // accumulators (dV, dK; dQ in kColA)
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------ prep
+// 128 rows of one head a block, 8 threads a row.
+__global__ void __launch_bounds__(256)
+attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restrict__ lse2, float* __restrict__ dsum,
+                 int2* __restrict__ ranges, AttnTileRange* __restrict__ tiles) {
+  __shared__ AttnTileRange part[8];
+  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, c = threadIdx.x & 7;
+  const size_t Lp = (size_t)q_tiles * kAttnTile;
+  AttnTileRange tr{0x7fffffff, 0, 0, 0x7fffffff, 0, {0, 0, 0}};
+#pragma unroll
+  for (int pass = 0; pass < 4; ++pass) {
+    const int l = blockIdx.x * kAttnTile + pass * 32 + (threadIdx.x >> 3);
+    const int2 keys = l < a.L ? key_range(a, b, l) : make_int2(0, 0);
+    const bool live = keys.x < keys.y;
+    float s = 0.f;
+    if (live && c * 8 < a.d) {
+      const uint4 x = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.dout.data) +
+                                                     b * a.dout.sb + h * a.dout.sh + l * a.dout.st)[c];
+      const uint4 y = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.out.data) + b * a.out.sb +
+                                                     h * a.out.sh + l * a.out.st)[c];
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+        s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (c == 0) {
+      lse2[bh * Lp + l] = live ? a.lse_in[(size_t)bh * a.L + l] * kLog2e : INFINITY;
+      dsum[bh * Lp + l] = s;
+      if (h == 0) ranges[b * Lp + l] = keys;
+    }
+    if (live) {
+      tr.lo = min(tr.lo, keys.x);
+      tr.hi = max(tr.hi, keys.y);
+      tr.flo = max(tr.flo, keys.x);
+      tr.fhi = min(tr.fhi, keys.y);
+    } else if (l < a.L && c == 0) {
+      ++tr.dead;
+    }
+  }
+  if (h != 0) return;
+  tr.lo = warp_min(tr.lo);
+  tr.hi = warp_max(tr.hi);
+  tr.flo = warp_max(tr.flo);
+  tr.fhi = warp_min(tr.fhi);
+  tr.dead = __reduce_add_sync(0xffffffffu, tr.dead);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = tr;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) {
+      tr.lo = min(tr.lo, part[w].lo);
+      tr.hi = max(tr.hi, part[w].hi);
+      tr.flo = max(tr.flo, part[w].flo);
+      tr.fhi = min(tr.fhi, part[w].fhi);
+      tr.dead += part[w].dead;
+    }
+    tiles[(size_t)b * q_tiles + blockIdx.x] = tr;
+  }
+}
+
+// The A operand of K step kk (16 of the 128 columns) of a P or dS that the
+// two warpgroups wrote into their halves of buffer `col`.
+__device__ __forceinline__ uint32_t a_col(uint32_t col, int kk) { return col + (kk >> 2) * 64 + (kk & 3) * 8; }
+
+// D (+)= A B^T, both K-major tiles of 128 rows x 64 channels.
+__device__ __forceinline__ void mma_rows(uint32_t d, const uint8_t* A, const uint8_t* B) {
+  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+  const uint32_t x = smem_u32(A), y = smem_u32(B);
+#pragma unroll
+  for (int kk = 0; kk < kAttnD / 16; ++kk)
+    umma_bf16(d, sw128_desc(x + kk * 32, 1024), sw128_desc(y + kk * 32, 1024), id, kk > 0);
+}
+// D (+)= A B, A in TMEM (128 x 128), B a tile of 128 rows x 64 channels.
+__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, const uint8_t* B, bool add) {
+  constexpr uint32_t id = idesc_bf16(128, kAttnD, false, true);
+  const uint32_t y = smem_u32(B);
+#pragma unroll
+  for (int kk = 0; kk < kAttnTile / 16; ++kk)
+    umma_bf16_ts(d, a_col(A, kk), sw128_desc(y + kk * 16 * 128, 1024), id, (add || kk > 0) ? 1u : 0u);
+}
+
+// ------------------------------------------------------------------ dK, dV
+struct DkvSmem {
+  uint8_t k[kTileBytes], v[kTileBytes];
+  uint8_t q[kStages][kTileBytes], g[kStages][kTileBytes];     // query and dout tiles
+  float lse2[kStages][kAttnTile], dsum[kStages][kAttnTile];
+  int2 range[kStages][kAttnTile];
+  uint32_t active[kMaxQTiles / 32], masked[kMaxQTiles / 32], dead[kMaxQTiles / 32];
+  uint64_t kv_full, q_full[kStages], q_empty[kStages];
+  uint64_t full[3], p_ready[2], ds_ready[2], drain;
+  int count[kThreads / 32];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kDkvSmem = sizeof(DkvSmem) + 1024;
+static_assert(kDkvSmem <= 227 * 1024, "shared memory");
+
+// Walks over the set bits of `active`, round after round (one per head).
+struct TileWalk {
+  const uint32_t* bits;
+  int words, w;
+  uint32_t cur;
+  int head;
+  __device__ TileWalk(const uint32_t* bits_, int words_, int n_active, int start)
+      : bits(bits_), words(words_), w(0), cur(0), head(0) {
+    if (n_active == 0) return;                                  // nothing to walk: next() is not called
+    cur = bits[0];
+    head = start / n_active;
+    int skip = start % n_active;                                // below n_active: ends before the last set bit
+    while (skip >= __popc(cur)) {
+      skip -= __popc(cur);
+      cur = bits[++w];
+    }
+    for (; skip > 0; --skip) cur &= cur - 1;
+  }
+  // the next tile (there is always one: the walk wraps to the next head)
+  __device__ int next() {
+    while (cur == 0) {
+      if (++w == words) {
+        w = 0;
+        ++head;
+      }
+      cur = bits[w];
+    }
+    const int t = w * 32 + __ffs(cur) - 1;
+    cur &= cur - 1;
+    return t;
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
+                const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
+                const __grid_constant__ AttnArgs a, int q_tiles, int k_tiles, int parts,
+                const float* __restrict__ lse2, const float* __restrict__ dsum, const int2* __restrict__ ranges,
+                const AttnTileRange* __restrict__ tiles, float* __restrict__ part_out) {
+  extern __shared__ uint8_t smem_raw[];
+  DkvSmem& sm = *reinterpret_cast<DkvSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned item = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int bk = item / k_tiles, kt = item % k_tiles, b = bk / a.K, kh = bk % a.K;
+  const int k0 = kt * kAttnTile, k1 = min(k0 + kAttnTile, a.N);
+  const int words = (q_tiles + 31) / 32;
+  const size_t Lp = (size_t)q_tiles * kAttnTile;
+  DevState* st = a.st;
+
+  // which query tiles see these keys, which of them need compares, which
+  // hold rows that see nothing
+  int mine = 0;
+  for (int w = warp; w < words; w += kThreads / 32) {
+    const int t = w * 32 + lane;
+    bool act = false, msk = false, ded = false;
+    if (t < q_tiles) {
+      const AttnTileRange r = tiles[(size_t)b * q_tiles + t];
+      act = r.lo < r.hi && r.lo < k1 && r.hi > k0;
+      msk = !(r.flo <= k0 && r.fhi >= k1);
+      ded = r.dead > 0;
+    }
+    const uint32_t wa = __ballot_sync(0xffffffffu, act), wm = __ballot_sync(0xffffffffu, msk),
+                   wd = __ballot_sync(0xffffffffu, ded);
+    if (lane == 0) {
+      sm.active[w] = wa;
+      sm.masked[w] = wm;
+      sm.dead[w] = wd;
+    }
+    mine += __popc(wa);
+  }
+  if (lane == 0) sm.count[warp] = mine;
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.kv_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.q_full[s], 1);
+      mbar_init(&sm.q_empty[s], 1);
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.p_ready[i], 256);
+      mbar_init(&sm.ds_ready[i], 256);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  int n_active = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) n_active += sm.count[w];
+  const long long all = (long long)n_active * a.G;
+  const int s0 = (int)(all * part / parts), n = (int)(all * (part + 1) / parts) - s0;   // steps of this CTA
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 0 && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ producer
+      mbar_arrive_expect_tx(&sm.kv_full, 2 * kTileBytes);
+      tma_load_tile(sm.k, mk, &sm.kv_full, k0, kh, b);
+      tma_load_tile(sm.v, mv, &sm.kv_full, k0, kh, b);
+      TileWalk walk(sm.active, words, n_active, s0);
+      for (int i = 0; i < n; ++i) {
+        const int s = i % kStages, t = walk.next(), h = kh * a.G + walk.head;
+        if (i >= kStages && !mbar_wait(&sm.q_empty[s], ((i / kStages) - 1) & 1, abort, st)) break;
+        const size_t at = ((size_t)b * a.H + h) * Lp + (size_t)t * kAttnTile;
+        mbar_arrive_expect_tx(&sm.q_full[s], 2 * kTileBytes + kAttnTile * 16);
+        tma_load_tile(sm.q[s], mq, &sm.q_full[s], t * kAttnTile, h, b);
+        tma_load_tile(sm.g[s], mg, &sm.q_full[s], t * kAttnTile, h, b);
+        bulk_load(sm.lse2[s], lse2 + at, kAttnTile * 4, &sm.q_full[s]);
+        bulk_load(sm.dsum[s], dsum + at, kAttnTile * 4, &sm.q_full[s]);
+        bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kAttnTile, kAttnTile * 8, &sm.q_full[s]);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issue
+      bool ok = n > 0 && __all_sync(0xffffffffu, mbar_wait(&sm.kv_full, 0, abort, st));
+      TileWalk walk(sm.active, words, n_active, s0);
+      auto issue_s = [&](int i) -> bool {                       // S_i: product 2 i
+        const int s = i % kStages, t = walk.next();
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st))) return false;
+        if (sm.dead[t >> 5] >> (t & 31) & 1) {                  // rows that may hold anything
+          zero_rows(sm.q[s], [&](int r) { return sm.lse2[s][r] == INFINITY; });
+          zero_rows(sm.g[s], [&](int r) { return sm.lse2[s][r] == INFINITY; });
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const int buf = (2 * i) % 3;
+          mma_rows(tmem + buf * 128, sm.k, sm.q[s]);
+          umma_commit(&sm.full[buf]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_dp = [&](int i) {                              // dP_i: product 2 i + 1
+        if (lane == 0) {
+          const int buf = (2 * i + 1) % 3;
+          mma_rows(tmem + buf * 128, sm.v, sm.g[i % kStages]);
+          umma_commit(&sm.full[buf]);
+        }
+        __syncwarp();
+      };
+      if (ok) ok = issue_s(0);
+      if (ok) issue_dp(0);
+      if (ok && n > 1) ok = issue_s(1);
+      for (int i = 0; ok && i < n; ++i) {
+        const int s = i % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.p_ready[i & 1], (i >> 1) & 1, abort, st))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          mma_cols(tmem + kColA, tmem + ((2 * i) % 3) * 128, sm.g[s], i > 0);
+        }
+        __syncwarp();
+        if (i + 1 < n) issue_dp(i + 1);                         // into the buffer dV_i reads from
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.ds_ready[i & 1], (i >> 1) & 1, abort, st))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          mma_cols(tmem + kColB, tmem + ((2 * i + 1) % 3) * 128, sm.q[s], i > 0);
+          umma_commit(&sm.q_empty[s]);
+        }
+        __syncwarp();
+        if (i + 2 < n) ok = issue_s(i + 2);                     // into the buffer dK_i reads from
+      }
+      if (lane == 0) {
+        umma_commit(&sm.drain);
+        drain_mma(&sm.drain, 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ------------------------------------------------------------ P and dS
+    const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int key = k0 + row;
+    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), neg = f2_pack(-1.f, -1.f);
+    bool ok = true;
+    if (n > 0) {
+      TileWalk walk(sm.active, words, n_active, s0);
+      for (int i = 0; i < n; ++i) {
+        const int s = i % kStages, t = walk.next();
+        const bool masked = sm.masked[t >> 5] >> (t & 31) & 1;
+        const uint32_t ts = tmem + lane_off + ((2 * i) % 3) * 128 + wg * 64;
+        const uint32_t td = tmem + lane_off + ((2 * i + 1) % 3) * 128 + wg * 64;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) ||
+            !__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * i) % 3], ((2 * i) / 3) & 1, abort, st))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t p[64];
+        tmem_ld64(ts, p);
+        // p = 2^(s c - lse2) of this key and the 64 queries of the columns
+        const float4* lp = reinterpret_cast<const float4*>(sm.lse2[s] + wg * 64);
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 m = lp[e];
+          float x[4];
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(p[4 * e]), __uint_as_float(p[4 * e + 1])), cc, f2_mul(f2_pack(m.x, m.y), neg)), x[0], x[1]);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(p[4 * e + 2]), __uint_as_float(p[4 * e + 3])), cc, f2_mul(f2_pack(m.z, m.w), neg)), x[2], x[3]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) p[4 * e + c] = __float_as_uint(ex2(x[c]));
+        }
+        if (masked) {
+          const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + wg * 64);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int4 r = rp[e];
+            if (key < r.x || key >= r.y) p[2 * e] = 0u;
+            if (key < r.z || key >= r.w) p[2 * e + 1] = 0u;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]));
+        tmem_st32(ts, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_ready[i & 1]);
+        // dS = P (dP - D)
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * i + 1) % 3], ((2 * i + 1) / 3) & 1, abort, st))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t g[64];
+        tmem_ld64(td, g);
+        const float4* dp = reinterpret_cast<const float4*>(sm.dsum[s] + wg * 64);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 m = dp[e];
+          const float ms[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float pv = __uint_as_float(p[4 * e + c]);
+            float ds = pv * (__uint_as_float(g[4 * e + c]) - ms[c]);
+            if (masked && pv == 0.f) ds = 0.f;                  // a value nobody sees may be NaN
+            g[4 * e + c] = __float_as_uint(ds);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+        tmem_st32(td, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.ds_ready[i & 1]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
+    }
+    tc_fence_after();
+    // warpgroup 0 stores dV, warpgroup 1 dK
+    if (ok) {
+      uint32_t o[64];
+      if (n > 0) {
+        tmem_ld64(tmem + lane_off + (wg == 0 ? kColA : kColB), o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) o[e] = 0u;
+      }
+      if (parts > 1) {
+        float4* dst = reinterpret_cast<float4*>(part_out + (((size_t)blockIdx.x * 2 + wg) * kAttnTile + row) * kAttnD);
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]), __uint_as_float(o[4 * v + 2]),
+                               __uint_as_float(o[4 * v + 3]));
+      } else if (key < a.N) {
+        const View& w = wg == 0 ? a.dv : a.dk;
+        __nv_bfloat16* dst =
+            reinterpret_cast<__nv_bfloat16*>(w.data) + b * w.sb + kh * w.sh + (int64_t)key * w.st;
+        store_row_bf16<8>(o, dst, wg == 0 ? 1.f : a.scale, 0, a.d);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    if (*abort)
+      for (int i = 0; i < 200; ++i) __nanosleep(1000);           // copies in flight land
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds up the parts of split key tiles, in order: 8 threads a row, 8
+// channels each.
+__global__ void __launch_bounds__(256)
+attn_dkv_join_kernel(const __grid_constant__ AttnArgs a, int k_tiles, int parts, const float* __restrict__ part_in) {
+  const long long idx = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+  if (idx >= 2ll * a.B * a.K * a.N) return;
+  const int c = threadIdx.x & 7, wg = (int)(idx & 1);
+  const int key = (int)((idx >> 1) % a.N), bk = (int)((idx >> 1) / a.N);
+  const long long item = (long long)bk * k_tiles + key / kAttnTile;
+  const float* src =
+      part_in + (((size_t)item * parts * 2 + wg) * kAttnTile + key % kAttnTile) * kAttnD + c * 8;
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < parts; ++p) {
+    const float4* x = reinterpret_cast<const float4*>(src + (size_t)p * 2 * kAttnTile * kAttnD);
+    const float4 u = x[0], v = x[1];
+    o[0] += u.x, o[1] += u.y, o[2] += u.z, o[3] += u.w, o[4] += v.x, o[5] += v.y, o[6] += v.z, o[7] += v.w;
+  }
+  if (c * 8 >= a.d) return;
+  const float f = wg == 0 ? 1.f : a.scale;
+  const View& w = wg == 0 ? a.dv : a.dk;
+  __nv_bfloat16* dst =
+      reinterpret_cast<__nv_bfloat16*>(w.data) + bk / a.K * w.sb + bk % a.K * w.sh + (int64_t)key * w.st + c * 8;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
+                                              pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
+}
+
+// ------------------------------------------------------------------ dQ
+struct DqSmem {
+  uint8_t q[kTileBytes], g[kTileBytes];
+  uint8_t k[kStages][kTileBytes], v[kStages][kTileBytes];
+  uint64_t q_full, kv_full[kStages], kv_empty[kStages];
+  uint64_t full[3], s_read[2], ds_ready[2], drain;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kDqSmem = sizeof(DqSmem) + 1024;
+static_assert(kDqSmem <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
+               const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
+               const __grid_constant__ AttnArgs a, int q_tiles, const float* __restrict__ lse2,
+               const float* __restrict__ dsum, const int2* __restrict__ ranges,
+               const AttnTileRange* __restrict__ tiles) {
+  extern __shared__ uint8_t smem_raw[];
+  DqSmem& sm = *reinterpret_cast<DqSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.x / q_tiles, qt = q_tiles - 1 - blockIdx.x % q_tiles;
+  const int b = bh / a.H, h = bh % a.H, kh = h / a.G;
+  const size_t Lp = (size_t)q_tiles * kAttnTile;
+  const AttnTileRange tr = tiles[(size_t)b * q_tiles + qt];
+  const int n = tr.lo < tr.hi ? (tr.hi - tr.lo + kAttnTile - 1) / kAttnTile : 0, base = n > 0 ? tr.lo : 0;
+  DevState* st = a.st;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_read[i], 256);
+      mbar_init(&sm.ds_ready[i], 256);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 0 && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ producer
+      mbar_arrive_expect_tx(&sm.q_full, 2 * kTileBytes);
+      tma_load_tile(sm.q, mq, &sm.q_full, qt * kAttnTile, h, b);
+      tma_load_tile(sm.g, mg, &sm.q_full, qt * kAttnTile, h, b);
+      for (int j = 0; j < n; ++j) {
+        const int s = j % kStages;
+        if (j >= kStages && !mbar_wait(&sm.kv_empty[s], ((j / kStages) - 1) & 1, abort, st)) break;
+        mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kTileBytes);
+        tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kAttnTile, kh, b);
+        tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kAttnTile, kh, b);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issue
+      bool ok = n > 0 && __all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, abort, st));
+      auto issue_s = [&](int j) -> bool {
+        const int s = j % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st))) return false;
+        const int n_valid = tr.hi - (base + j * kAttnTile);
+        if (n_valid < kAttnTile) {                              // K rows behind the union of the ranges
+          zero_rows(sm.k[s], [&](int r) { return r >= n_valid; });
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const int buf = (2 * j) % 3;
+          mma_rows(tmem + buf * 128, sm.q, sm.k[s]);
+          umma_commit(&sm.full[buf]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_dp = [&](int j) {
+        if (lane == 0) {
+          const int buf = (2 * j + 1) % 3;
+          mma_rows(tmem + buf * 128, sm.g, sm.v[j % kStages]);
+          umma_commit(&sm.full[buf]);
+        }
+        __syncwarp();
+      };
+      if (ok) ok = issue_s(0);
+      if (ok) issue_dp(0);
+      if (ok && n > 1) ok = issue_s(1);
+      for (int j = 0; ok && j < n; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_read[j & 1], (j >> 1) & 1, abort, st))) break;
+        tc_fence_after();
+        if (j + 1 < n) issue_dp(j + 1);                         // into the buffer S_j was read from
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.ds_ready[j & 1], (j >> 1) & 1, abort, st))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          mma_cols(tmem + kColA, tmem + ((2 * j + 1) % 3) * 128, sm.k[j % kStages], j > 0);
+          umma_commit(&sm.kv_empty[j % kStages]);
+        }
+        __syncwarp();
+        if (j + 2 < n) ok = issue_s(j + 2);                     // into the buffer dQ_j reads from
+      }
+      if (lane == 0) {
+        umma_commit(&sm.drain);
+        drain_mma(&sm.drain, 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ------------------------------------------------------------ dS
+    const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int l = qt * kAttnTile + row;                         // below Lp
+    const float m = lse2[(size_t)bh * Lp + l], D = dsum[(size_t)bh * Lp + l];
+    const int2 keys = ranges[b * Lp + l];
+    const bool live = keys.x < keys.y;
+    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), mm = f2_pack(-m, -m);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t ts = tmem + lane_off + ((2 * j) % 3) * 128 + wg * 64;
+      const uint32_t td = tmem + lane_off + ((2 * j + 1) % 3) * 128 + wg * 64;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * j) % 3], ((2 * j) / 3) & 1, abort, st))) { ok = false; break; }
+      tc_fence_after();
+      uint32_t p[64];
+      tmem_ld64(ts, p);
+      tc_fence_before();
+      mbar_arrive(&sm.s_read[j & 1]);
+      const int first = keys.x - (base + j * kAttnTile) - wg * 64, last = keys.y - (base + j * kAttnTile) - wg * 64;
+      const bool masked = __any_sync(0xffffffffu, first > 0 || last < 64);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1])), cc, mm), x0, x1);
+        p[2 * e] = __float_as_uint(ex2(x0));
+        p[2 * e + 1] = __float_as_uint(ex2(x1));
+      }
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e < first || e >= last) p[e] = 0u;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * j + 1) % 3], ((2 * j + 1) / 3) & 1, abort, st))) { ok = false; break; }
+      tc_fence_after();
+      uint32_t g[64], pk[32];
+      tmem_ld64(td, g);
+#pragma unroll
+      for (int e = 0; e < 64; ++e) {
+        const float pv = __uint_as_float(p[e]);
+        float ds = pv * (__uint_as_float(g[e]) - D);
+        if (masked && pv == 0.f) ds = 0.f;                      // a value nobody sees may be NaN
+        g[e] = __float_as_uint(ds);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+      tmem_st32(td, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sm.ds_ready[j & 1]);
+    }
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
+    tc_fence_after();
+    if (ok) {
+      uint32_t o[32];                                           // each warpgroup stores 32 channels
+      if (n > 0) {
+        tmem_ld32(tmem + lane_off + kColA + wg * 32, o);
+        tmem_wait_ld();
+      }
+      if (n == 0 || !live) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      if (l < a.L) {
+        __nv_bfloat16* dst =
+            reinterpret_cast<__nv_bfloat16*>(a.dq.data) + b * a.dq.sb + h * a.dq.sh + (int64_t)l * a.dq.st;
+        store_row_bf16<4>(o, dst, a.scale, wg * 32, a.d);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    if (*abort)
+      for (int i = 0; i < 200; ++i) __nanosleep(1000);           // copies in flight land
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+// Splits of a key tile's queries: as for the forward, waves of CTAs times
+// their steps plus about three steps of start and end.
+AttnBwdPlan attn_bwd_plan(const httm_attention& a) {
+  AttnBwdPlan p{};
+  p.q_tiles = (a.q_len + kAttnTile - 1) / kAttnTile;
+  p.k_tiles = (a.kv_len + kAttnTile - 1) / kAttnTile;
+  p.Lp = p.q_tiles * kAttnTile;
+  const long long items = (long long)a.batch * a.kv_heads * p.k_tiles;
+  const long long steps = (long long)(a.heads / a.kv_heads) * p.q_tiles;
+  p.kv_parts = 1;
+  double best = 0;
+  for (int n = 1; n <= std::min<long long>(16, std::max<long long>(1, steps)) && items > 0; ++n) {
+    if (n > 1 && items * n > 4 * kSMs) break;
+    const long long waves = (items * n + kSMs - 1) / kSMs;
+    const double cost = (double)waves * ((steps + n - 1) / n + 3) + (n > 1 ? 4 + n / 4.0 : 0);
+    if (n == 1 || cost < best) best = cost, p.kv_parts = n;
+  }
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += up256(bytes);
+    return o;
+  };
+  p.stat = take((size_t)2 * a.batch * a.heads * p.Lp * sizeof(float));
+  p.range = take((size_t)a.batch * p.Lp * sizeof(int2));
+  p.tiles = take((size_t)a.batch * p.q_tiles * sizeof(AttnTileRange));
+  p.part = take(p.kv_parts > 1 ? (size_t)items * p.kv_parts * 2 * kAttnTile * kAttnD * sizeof(float) : 0);
+  p.total = off;
+  return p;
+}
+
+cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, cudaStream_t s) {
+  char* w = static_cast<char*>(ws);
+  float* lse2 = reinterpret_cast<float*>(w + p.stat);
+  float* dsum = lse2 + (size_t)a.B * a.H * p.Lp;
+  int2* ranges = reinterpret_cast<int2*>(w + p.range);
+  AttnTileRange* tiles = reinterpret_cast<AttnTileRange*>(w + p.tiles);
+  float* part = reinterpret_cast<float*>(w + p.part);
+  AttnMap mq, mg, mk, mv;
+  // with no queries (or no keys) nothing is loaded through their maps
+  const void* any = a.L > 0 ? a.q.data : a.k.data;
+  if (!attn_map(&mq, a.q, any, a.d, a.L, a.H, a.B) || !attn_map(&mg, a.dout, any, a.d, a.L, a.H, a.B) ||
+      !attn_map(&mk, a.k, any, a.d, a.N, a.K, a.B) || !attn_map(&mv, a.v, any, a.d, a.N, a.K, a.B))
+    return cudaErrorInvalidValue;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDkvSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem)) != cudaSuccess)
+    return e;
+  if (p.q_tiles > 0) {
+    attn_prep_kernel<<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, lse2, dsum, ranges, tiles);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (p.k_tiles > 0) {
+    const long long items = (long long)a.B * a.K * p.k_tiles;
+    attn_dkv_kernel<<<(unsigned)(items * p.kv_parts), kThreads, kDkvSmem, s>>>(
+        mq, mg, mk, mv, a, p.q_tiles, p.k_tiles, p.kv_parts, lse2, dsum, ranges, tiles, part);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (p.kv_parts > 1) {
+      const long long rows = 2ll * a.B * a.K * a.N;
+      attn_dkv_join_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, s>>>(a, p.k_tiles, p.kv_parts, part);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  }
+  if (p.q_tiles > 0)
+    attn_dq_kernel<<<(unsigned)((long long)a.B * a.H * p.q_tiles), kThreads, kDqSmem, s>>>(mq, mg, mk, mv, a, p.q_tiles,
+                                                                                         lse2, dsum, ranges, tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace httm

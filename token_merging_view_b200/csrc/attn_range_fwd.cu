@@ -1,0 +1,447 @@
+// Attention over key ranges, forward: out_i = sum_j P_ij V_j over the keys
+// j in [begin_i, end_i), and the row's log-sum-exp.
+//
+// Query rows: the G query heads that share a key head are packed next to
+// each other (row r = query r / G, head r % G), so K and V are read once for
+// all of them and a single token of a grouped model fills G rows of a tile.
+// A work item is up to 256 such rows of one key head -- two 128-row tiles,
+// or one when there are no more -- against the union of their key ranges.
+//
+// 12 warps: warp 0 loads K/V tiles of 128 keys by TMA into a ring of four;
+// warp 1 issues tcgen05.mma (S = Q K^T from shared memory, then O += P V
+// with P read from TMEM); warps 4..7 and 8..11 are the softmax of tiles 0
+// and 1, one row a thread.  TMEM: a ring of three 128-column S buffers (P
+// overwrites half of its S), O_0 and O_1 of 64 columns: 512.  The i-th S
+// product goes to buffer i % 3 and is issued right behind the P V product
+// that frees it, so the tensor core works on one tile during the other's
+// softmax.  Scores are exponentiated against a maximum in use that is raised
+// (and O rescaled) only when a tile's sum passes 2^16.  Bound by the exp
+// unit together with the cost of the N = 64 MMAs, as the layer's dense
+// attention is; with few rows by the memory that K and V come from.
+//
+// Splits: with fewer items than SMs (single tokens), or a last wave that
+// would run mostly empty, each item's keys are cut in `parts` ranges of
+// whole tiles; the parts leave unnormalised sums and maxima, which
+// attn_join_kernel adds up in order.
+//
+// Masks: a tile that every row of a warp sees whole takes no compares.
+// Keys outside the union of the item's ranges never enter: whole tiles are
+// not loaded, and in the last tile the V rows behind the union are zeroed
+// (a zero probability times a NaN there would not be zero).
+#include <algorithm>
+#include <mutex>
+
+#include "attn_ops.cuh"
+
+namespace httm {
+namespace {
+
+using namespace tc;
+
+constexpr int kStages = 4;
+constexpr int kThreads = 384;
+constexpr uint32_t kColO = 384;           // O_t at kColO + 64 t; S ring at 0, 128, 256
+constexpr int kPartStride = 68;           // floats of a partial row: O (64), sum, max in use, 2 unused
+
+struct FwdSmem {
+  uint8_t q[2][kTileBytes];
+  uint8_t k[kStages][kTileBytes];
+  uint8_t v[kStages][kTileBytes];
+  uint64_t q_full;
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[3], p_full[2], o_done[2];
+  uint64_t drain;
+  int lo[8], hi[8];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = sizeof(FwdSmem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(kThreads, 1)
+attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
+                      const __grid_constant__ AttnArgs a, int row_tiles, int parts, float* __restrict__ part_out) {
+  extern __shared__ uint8_t smem_raw[];
+  FwdSmem& sm = *reinterpret_cast<FwdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // later rows usually see more keys (causal): they go first
+  const unsigned item = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int bk = item / row_tiles, rt = row_tiles - 1 - item % row_tiles;
+  const int b = bk / a.K, kh = bk % a.K;
+  const int rows = a.L * a.G - rt * 256;             // rows from this item's first on
+  const int n_t = rows > 128 ? 2 : 1;
+  DevState* st = a.st;
+
+  // this thread's query row (softmax threads): its head, query and keys
+  const int t = warp >= 8 ? 1 : 0;
+  const int row = (warp & 3) * 32 + lane;            // row inside the tile = TMEM lane
+  const int r_item = t * 128 + row;
+  const bool in_item = warp >= 4 && r_item < rows;
+  const int r_all = rt * 256 + r_item;
+  const int l = in_item ? r_all / a.G : 0, head = in_item ? kh * a.G + (r_all - l * a.G) : 0;
+  int2 keys = in_item ? key_range(a, b, l) : make_int2(0, 0);
+  if (warp >= 4) {
+    const bool live = keys.x < keys.y;
+    const int lo = warp_min(live ? keys.x : 0x7fffffff), hi = warp_max(live ? keys.y : 0);
+    if (lane == 0) {
+      sm.lo[warp - 4] = lo;
+      sm.hi[warp - 4] = hi;
+    }
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, 128 * n_t);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.o_done[i], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  int lo = 0x7fffffff, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo = min(lo, sm.lo[i]);
+    hi = max(hi, sm.hi[i]);
+  }
+  // this part's tiles: keys [base, base + 128 n_kv) of [lo, hi)
+  const int n_all = hi > lo ? (hi - lo + kAttnTile - 1) / kAttnTile : 0;
+  const int j0 = (int)((long long)n_all * part / parts);
+  const int n_kv = (int)((long long)n_all * (part + 1) / parts) - j0;
+  const int base = n_all > 0 ? lo + j0 * kAttnTile : 0;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ producer
+      for (int j = 0; j < n_kv; ++j) {
+        const int s = j % kStages;
+        if (j >= kStages && !mbar_wait(&sm.kv_empty[s], ((j / kStages) - 1) & 1, abort, st)) break;
+        mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kTileBytes);
+        tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kAttnTile, kh, b);
+        tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kAttnTile, kh, b);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t id_o = idesc_bf16(128, kAttnD, false, true);
+      const int n_prod = n_t * n_kv;                 // S products: i = n_t j + tile
+      bool ok = n_kv > 0 && __all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, abort, st));
+      // product i: waits for its K/V tile if it is the tile's first
+      auto issue_qk = [&](int i) -> bool {
+        const int j = n_t == 2 ? i >> 1 : i, tile = n_t == 2 ? i & 1 : 0, s = j % kStages;
+        if (tile == 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st))) return false;
+          const int n_valid = hi - (base + j * kAttnTile);
+          if (n_valid < kAttnTile) {                 // V rows behind the union of the ranges
+            zero_rows(sm.v[s], [&](int r) { return r >= n_valid; });
+            fence_async_smem();
+            __syncwarp();
+          }
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t qa = smem_u32(sm.q[tile]), ka = smem_u32(sm.k[s]), col = tmem + (i % 3) * 128;
+#pragma unroll
+          for (int kk = 0; kk < kAttnD / 16; ++kk)
+            umma_bf16(col, sw128_desc(qa + kk * 32, 1024), sw128_desc(ka + kk * 32, 1024), id_s, kk > 0);
+          umma_commit(&sm.s_full[i % 3]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int i = 0; ok && i < min(3, n_prod); ++i) ok = issue_qk(i);
+      for (int i = 0; ok && i < n_prod; ++i) {
+        const int j = n_t == 2 ? i >> 1 : i, tile = n_t == 2 ? i & 1 : 0, s = j % kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_full[tile], j & 1, abort, st));
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t va = smem_u32(sm.v[s]), pc = tmem + (i % 3) * 128, oc = tmem + kColO + tile * 64;
+#pragma unroll
+          for (int kk = 0; kk < kAttnTile / 16; ++kk)
+            umma_bf16_ts(oc, pc + kk * 8, sw128_desc(va + kk * 16 * 128, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&sm.o_done[tile]);
+          if (tile == n_t - 1) umma_commit(&sm.kv_empty[s]);
+        }
+        __syncwarp();
+        if (i + 3 < n_prod) ok = issue_qk(i + 3);
+      }
+      if (lane == 0) {                               // every MMA ends before TMEM is released
+        umma_commit(&sm.drain);
+        drain_mma(&sm.drain, 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // -------------------------------------------------------------- softmax
+    if (t < n_t) {
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t to = tmem + lane_off + kColO + t * 64;      // this row of O_t
+      const bool live = keys.x < keys.y;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      // the row's queries into the swizzled tile (zeros behind d, and for
+      // rows that see nothing, whatever memory holds there)
+      {
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q.data) + b * a.q.sb + head * a.q.sh +
+                                   (int64_t)l * a.q.st;
+        uint8_t* dst = sm.q[t] + row * 128;
+        uint4 x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          x[c] = live && c * 8 < a.d ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(dst)[c ^ (row & 7)] = x[c];
+        fence_async_smem();
+        mbar_arrive(&sm.q_full);
+      }
+      float m_used = -INFINITY, sum = 0.f;
+      bool ok = true;
+      for (int j = 0; j < n_kv; ++j) {
+        const int i = n_t * j + t, buf = i % 3;                  // S product and its ring buffer
+        const uint32_t ts = tmem + lane_off + buf * 128;         // this row of S, then of P
+        // waits are made warp-uniform: tcgen05.ld/st below need every lane
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[buf], (i / 3) & 1, abort, st))) { ok = false; break; }
+        tc_fence_after();
+        const int first = keys.x - (base + j * kAttnTile), last = keys.y - (base + j * kAttnTile);
+        bool pv_done = j == 0;                                   // PV(t, j-1) seen complete
+        const bool sees = live && first < kAttnTile && last > 0;
+        if (!__any_sync(0xffffffffu, sees)) {
+          // none of this warp's rows sees this tile: P = 0 (rows that are
+          // never stored may keep what is there)
+          if (warp_live) {
+            uint32_t z[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z[e] = 0u;
+            tmem_st32(ts, z);
+            tmem_st32(ts + 32, z);
+          }
+        } else {
+          uint32_t sr[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_wait_ld();
+          if (__any_sync(0xffffffffu, first > 0 || last < kAttnTile)) {
+#pragma unroll
+            for (int e = 0; e < kAttnTile; ++e)
+              if (e < first || e >= last) sr[e] = __float_as_uint(-INFINITY);
+          }
+          // p = 2^(s c - m) against the maximum in use.  Sums above 2^16
+          // (always so on a row's first tile, where m = -inf) make the warp
+          // raise the maximum, rescale O and the sum, and redo the tile.
+          const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2);
+          float rsum = 0.f, m_ref = m_used;
+          for (int pass = 0; pass < 2; ++pass) {
+            const unsigned long long mm = f2_pack(-m_ref, -m_ref);
+            unsigned long long rs[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rs[e] = 0ull;            // (0.f, 0.f)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float s0 = __uint_as_float(sr[c * 64 + 2 * e]), s1 = __uint_as_float(sr[c * 64 + 2 * e + 1]);
+                const unsigned long long xp = f2_fma(f2_pack(s0, s1), cc, mm);
+                float x0, x1;
+                f2_unpack(xp, x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                rs[e & 3] = f2_add(rs[e & 3], f2_pack(p0, p1));
+                pk[e] = pack_bf16(p0, p1);
+              }
+              tmem_st32(ts + c * 32, pk);
+            }
+            float r0, r1, r2, r3, r4, r5, r6, r7;
+            f2_unpack(rs[0], r0, r1);
+            f2_unpack(rs[1], r2, r3);
+            f2_unpack(rs[2], r4, r5);
+            f2_unpack(rs[3], r6, r7);
+            rsum = ((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7));
+            if (pass == 1) break;
+            // rows that see nothing never ask; NaN sums count as large
+            const bool need = live && !(rsum <= 65536.f);
+            if (!__any_sync(0xffffffffu, need)) break;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              mx[e & 3] = max3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+            const float m_new = fmaxf(m_used, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale_log2);
+            // a row with nothing yet: reference 0, its P and sum stay 0
+            m_ref = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_ref);
+            if (j > 0) {
+              if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (j - 1) & 1, abort, st))) {
+                ok = false;
+                break;
+              }
+              pv_done = true;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t o[32];
+                tmem_ld32(to + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(to + c * 32, o);
+              }
+            }
+            sum *= alpha;
+            m_used = m_new;
+          }
+          if (!ok) break;
+          sum += rsum;
+        }
+        // no arrival for step j before PV(t, j-1) is complete: every parity
+        // wait on o_done is then at most one phase behind, and no warp can
+        // arrive twice before a slower one of its warpgroup arrives once
+        if (!pv_done && !__all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (j - 1) & 1, abort, st))) {
+          ok = false;
+          break;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[t]);
+      }
+      if (ok && n_kv > 0)
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (n_kv - 1) & 1, abort, st));
+      tc_fence_after();
+      if (ok && parts > 1) {
+        // unnormalised sums, the row sum and the maximum in use; rows are
+        // counted without the padding of a last tile
+        const int item_rows = min(a.L * a.G, 256);
+        float* dst = part_out + ((size_t)blockIdx.x * item_rows + (in_item ? r_item : 0)) * kPartStride;
+        if (n_kv > 0) {
+          uint32_t o[64];
+          tmem_ld64(to, o);
+          if (in_item) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              reinterpret_cast<float4*>(dst)[v] =
+                  make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]), __uint_as_float(o[4 * v + 2]),
+                              __uint_as_float(o[4 * v + 3]));
+          }
+        }
+        if (in_item) {
+          dst[kAttnD] = sum;
+          dst[kAttnD + 1] = m_used;
+        }
+      } else if (ok) {
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + head * a.out.sh +
+                             (int64_t)l * a.out.st;
+        if (n_kv > 0) {
+          uint32_t o[64];
+          tmem_ld64(to, o);
+          if (in_item && live) store_row_bf16<8>(o, dst, 1.f / sum, 0, a.d);
+        }
+        if (in_item && !live)
+          for (int v = 0; v < a.d / 8; ++v) reinterpret_cast<uint4*>(dst)[v] = make_uint4(0, 0, 0, 0);
+        if (in_item && a.lse)
+          a.lse[((size_t)b * a.H + head) * a.L + l] = live ? (m_used + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    if (*abort) {
+      // let TMA copies still in flight land before the shared memory goes away
+      for (int i = 0; i < 200; ++i) __nanosleep(1000);
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds up the parts of every row: with M the largest maximum in use, O =
+// sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), in part order.  16 threads
+// a row, four channels each.
+__global__ void __launch_bounds__(256)
+attn_join_kernel(const __grid_constant__ AttnArgs a, int row_tiles, int parts, const float* __restrict__ part_in) {
+  const int rows = a.L * a.G, item_rows = min(rows, 256);
+  const long long idx = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (idx >= (long long)a.B * a.K * rows) return;
+  const int c = threadIdx.x & 15;
+  const int bk = (int)(idx / rows), r = (int)(idx % rows), rt = r / 256;
+  const long long item = (long long)bk * row_tiles + (row_tiles - 1 - rt);
+  const float* src = part_in + ((size_t)item * parts * item_rows + (r - rt * 256)) * kPartStride;
+  const size_t step = (size_t)item_rows * kPartStride;
+  float mx = -INFINITY, sum = 0.f;
+  for (int p = 0; p < parts; ++p) mx = fmaxf(mx, src[p * step + kAttnD + 1]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < parts; ++p) {
+    const float m = src[p * step + kAttnD + 1];
+    if (m == -INFINITY) continue;                    // saw none of its keys
+    const float w = ex2(m - mx);
+    const float4 x = reinterpret_cast<const float4*>(src + p * step)[c];
+    sum = fmaf(src[p * step + kAttnD], w, sum);
+    o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+  }
+  const int l = r / a.G, head = (bk % a.K) * a.G + (r - l * a.G), b = bk / a.K;
+  const int2 keys = key_range(a, b, l);
+  const bool live = keys.x < keys.y;
+  const float inv = live ? 1.f / sum : 0.f;
+  if (!live) o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c * 4 < a.d) {
+    __nv_bfloat16* dst =
+        reinterpret_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + head * a.out.sh + (int64_t)l * a.out.st;
+    reinterpret_cast<uint2*>(dst)[c] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
+  if (c == 0 && a.lse)
+    a.lse[((size_t)b * a.H + head) * a.L + l] = live ? (mx + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+}  // namespace
+
+// Parts: the split that keeps the SMs busiest by a count of tile steps.  A
+// CTA costs its tiles plus about three tiles' time of start and end, the
+// join about four once plus its partial rows; `parts` minimises waves x cost.
+AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
+  AttnFwdPlan p{};
+  const int G = a.heads / a.kv_heads;
+  p.rows = a.q_len * G;
+  p.row_tiles = (p.rows + 255) / 256;
+  p.items = (long long)a.batch * a.kv_heads * p.row_tiles;
+  const long long tiles = (a.kv_len + kAttnTile - 1) / kAttnTile;
+  p.parts = 1;
+  double best = 0;
+  const long long most = std::min<long long>(kAttnMaxParts, std::max<long long>(1, tiles));
+  for (int n = 1; n <= most && p.items > 0; ++n) {
+    if (n > 1 && p.items * n > 16 * kSMs) break;
+    const long long waves = (p.items * n + kSMs - 1) / kSMs;
+    const double cost = (double)waves * ((tiles + n - 1) / n + 3) + (n > 1 ? 4 + n / 16.0 : 0);
+    if (n == 1 || cost < best) best = cost, p.parts = n;
+  }
+  p.part_bytes = p.parts > 1 ? (size_t)p.items * p.parts * std::min(p.rows, 256) * kPartStride * 4 : 0;
+  return p;
+}
+
+cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s) {
+  AttnMap mk, mv;
+  // without keys nothing is loaded through their maps
+  if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B) || !attn_map(&mv, a.v, a.q.data, a.d, a.N, a.K, a.B))
+    return cudaErrorInvalidValue;
+  cudaError_t e =
+      cudaFuncSetAttribute(attn_range_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  attn_range_fwd_kernel<<<(unsigned)(p.items * p.parts), kThreads, kSmemBytes, s>>>(mk, mv, a, p.row_tiles, p.parts,
+                                                                                    static_cast<float*>(ws));
+  if ((e = cudaGetLastError()) != cudaSuccess || p.parts == 1) return e;
+  const long long rows = (long long)a.B * a.K * p.rows;
+  attn_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a, p.row_tiles, p.parts, static_cast<float*>(ws));
+  return cudaGetLastError();
+}
+
+}  // namespace httm

@@ -1,0 +1,615 @@
+// The norms before and after a block, fused with its gate and residual:
+//   y = rs * x + gate * Post(f)          (stored in the stream's type)
+//   z = Pre(y as stored)                 (stored in the branch's type)
+// and their gradients.  With n = (v - mean) * r the normalised row (mean = 0
+// for RMSNorm) and u = dz * weight,
+//   dv = r * (u - mean(u) - n * mean(u * n))      (no mean(u) for RMSNorm).
+//
+// Bound by memory: forward reads x and f once and writes y and z once (8
+// bytes an element in bf16), backward reads dy, dz, f, y and writes dx, df
+// (12 bytes).  A row stays in registers between its two norms; the mean is
+// taken before the squares, so the variance does not cancel.
+//
+// Threads: a row belongs to NT threads, each with V vectors of 8 channels.
+// Forward uses one warp a row up to 1,024 channels (no block barriers).
+// Backward keeps the sums of up to five parameter gradients in registers
+// while a thread group walks over its rows, so it spreads a row over more
+// threads; each group writes one row of partial sums, which a second kernel
+// adds up in a fixed order (no atomics: the result does not depend on the
+// schedule).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace httm {
+namespace {
+
+constexpr int kMaxChannels = 8192;
+constexpr int kMaxGates = 1024;
+
+struct NormArgs {
+  const void *x, *f, *y, *dy, *dz;      // x: forward only
+  void *y_out, *z, *dx, *df;
+  int64_t sx, sf, sy, sz, sdy, sdz, sdx, sdf;
+  const float *gate, *post_w, *post_b, *pre_w, *pre_b;
+  float *stats, *partial;
+  int64_t rows, gate_rows;              // rows sharing a gate row
+  int C, gates;
+  int post, pre;
+  float post_eps, pre_eps, rs;
+  int chunks;                           // backward: thread groups per gate group
+  unsigned want;                        // backward: bit k = parameter gradient k is wanted
+};
+enum { kGate = 0, kPostW, kPostB, kPreW, kPreB, kNumGrads };
+
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// The channels of a thread.  VEC: vector v covers 8 neighbouring channels,
+// in 16-byte accesses (channels a multiple of 8, rows aligned); else the 8
+// are NT apart, so that neighbouring threads touch neighbouring elements.
+template <int NT, bool VEC>
+struct Cols {
+  int t, C;
+  __device__ __forceinline__ int at(int v, int e) const { return VEC ? (v * NT + t) * 8 + e : (v * 8 + e) * NT + t; }
+  __device__ __forceinline__ bool live(int v, int e) const { return at(v, VEC ? 0 : e) < C; }
+  // elements behind the row's end read as `fill`
+  template <class T>
+  __device__ __forceinline__ void load(const T* row, int v, float (&r)[8], float fill = 0.f) const {
+    if constexpr (VEC) {
+      if (live(v, 0)) {
+        load8(row + at(v, 0), r);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = fill;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = live(v, e) ? to_f(row[at(v, e)]) : fill;
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void store(T* row, int v, const float (&r)[8]) const {
+    if constexpr (VEC) {
+      if (live(v, 0)) store8(row + at(v, 0), r);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (live(v, e)) row[at(v, e)] = from_f<T>(r[e]);
+    }
+  }
+};
+
+// Sum over the NT threads of a row (all of them get it).  NT = 32: shuffles;
+// more: one row per block, through `tmp` (2 x 32 floats, used in turn so one
+// barrier per sum is enough).
+template <int NT, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*tmp)[K][32], int& turn) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+  if constexpr (NT > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) tmp[turn][k][warp] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < NT / 32 ? tmp[turn][k][lane] : 0.f);
+    turn ^= 1;
+  }
+}
+
+// n = (v - mean) * r in place; returns mean and r.
+template <int NT, bool VEC, int V>
+__device__ __forceinline__ void normalise(float (&v)[V][8], const Cols<NT, VEC>& cols, int kind, float eps, float inv_c,
+                                          float (*tmp)[1][32], int& turn, float& mean, float& r) {
+  mean = 0.f;
+  float s[1];
+  if (kind == HTTM_NORM_LAYER) {
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] += v[i][e];            // 0 behind the row's end
+    row_sums<NT, 1>(s, tmp, turn);
+    mean = s[0] * inv_c;
+  }
+  s[0] = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[i][e] = cols.live(i, e) ? v[i][e] - mean : 0.f;
+      s[0] = fmaf(v[i][e], v[i][e], s[0]);
+    }
+  row_sums<NT, 1>(s, tmp, turn);
+  r = rsqrtf(fmaf(s[0], inv_c, eps));
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] *= r;
+}
+
+template <int NT, bool VEC, int V>
+__device__ __forceinline__ void affine(float (&v)[V][8], const Cols<NT, VEC>& cols, const float* w, const float* b) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float g[8], o[8];
+    if (w) {
+      cols.load(w, i, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= g[e];
+    }
+    if (b) {
+      cols.load(b, i, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += o[e];
+    }
+  }
+}
+
+template <class TX, class TF, int NT, int V, bool VEC>
+__global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs a) {
+  constexpr int kRows = NT > 32 ? 1 : 4;                      // rows per block (barriers need one)
+  __shared__ float tmp[2][1][32];
+  int turn = 0;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
+  if (row >= a.rows) return;                                  // whole warps: NT is a multiple of 32
+  const Cols<NT, VEC> cols{(int)(threadIdx.x % NT), a.C};
+  const float inv_c = 1.f / (float)a.C;
+  float f[V][8], y[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) cols.load(static_cast<const TX*>(a.x) + row * a.sx, i, y[i]);
+  if (a.f) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) cols.load(static_cast<const TF*>(a.f) + row * a.sf, i, f[i]);
+  }
+  if (a.post != HTTM_NORM_NONE) {
+    float mean, r;
+    normalise<NT, VEC, V>(f, cols, a.post, a.post_eps, inv_c, tmp, turn, mean, r);
+    if (a.stats && cols.t == 0) {
+      a.stats[row] = mean;
+      a.stats[a.rows + row] = r;
+    }
+    affine<NT, VEC, V>(f, cols, a.post_w, a.post_b);
+  }
+  if (a.gate) {
+    const float* g = a.gate + (row / a.gate_rows) * a.C;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float gv[8];
+      cols.load(g, i, gv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= gv[e];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[i][e] = a.f ? fmaf(a.rs, y[i][e], f[i][e]) : a.rs * y[i][e];
+      y[i][e] = to_f(from_f<TX>(y[i][e]));                    // the norm reads the stream as it is stored
+    }
+  if (a.y_out) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) cols.store(static_cast<TX*>(a.y_out) + row * a.sy, i, y[i]);
+  }
+  if (a.pre != HTTM_NORM_NONE) {
+    float mean, r;
+    normalise<NT, VEC, V>(y, cols, a.pre, a.pre_eps, inv_c, tmp, turn, mean, r);
+    if (a.stats && cols.t == 0) {
+      a.stats[2 * a.rows + row] = mean;
+      a.stats[3 * a.rows + row] = r;
+    }
+    affine<NT, VEC, V>(y, cols, a.pre_w, a.pre_b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) cols.store(static_cast<TF*>(a.z) + row * a.sz, i, y[i]);
+  }
+}
+
+// Backward: thread group g of gate group q walks over its share of that
+// group's rows with 8 channels a thread.
+template <class TX, class TF, int NT, bool VEC>
+__global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_grad_kernel(NormArgs a) {
+  constexpr int kGroups = NT > 32 ? 1 : 4;                    // thread groups per block (barriers need one)
+  __shared__ float tmp[2][2][32];
+  int turn = 0;
+  const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / NT;
+  const int n_gates = max(1, a.gates);
+  if (group >= (int64_t)n_gates * a.chunks) return;
+  const Cols<NT, VEC> cols{(int)(threadIdx.x % NT), a.C};
+  const float inv_c = 1.f / (float)a.C;
+  const int gq = (int)(group / a.chunks), chunk = (int)(group % a.chunks);
+  const int64_t r0 = gq * a.gate_rows + a.gate_rows * chunk / a.chunks;
+  const int64_t r1 = gq * a.gate_rows + a.gate_rows * (chunk + 1) / a.chunks;
+
+  float gate[8], post_w[8], pre_w[8], post_b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) gate[e] = post_w[e] = pre_w[e] = 1.f, post_b[e] = 0.f;
+  if (a.gate) cols.load(a.gate + (int64_t)gq * a.C, 0, gate);
+  if (a.post_w) cols.load(a.post_w, 0, post_w);
+  if (a.post_b) cols.load(a.post_b, 0, post_b);
+  if (a.pre_w) cols.load(a.pre_w, 0, pre_w);
+  float acc[kNumGrads][8];
+#pragma unroll
+  for (int k = 0; k < kNumGrads; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+
+  for (int64_t row = r0; row < r1; ++row) {
+    float g[8], f[8], y[8], dz[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = f[e] = 0.f;
+    if (a.dy) cols.load(static_cast<const TX*>(a.dy) + row * a.sdy, 0, g);
+    if (a.f) cols.load(static_cast<const TF*>(a.f) + row * a.sf, 0, f);
+    if (a.pre != HTTM_NORM_NONE) {
+      cols.load(static_cast<const TX*>(a.y) + row * a.sy, 0, y);
+      cols.load(static_cast<const TF*>(a.dz) + row * a.sdz, 0, dz);
+      const float mean = a.pre == HTTM_NORM_LAYER ? a.stats[2 * a.rows + row] : 0.f, r = a.stats[3 * a.rows + row];
+      float s[2] = {0.f, 0.f}, u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = cols.live(0, e) ? (y[e] - mean) * r : 0.f;
+        u[e] = dz[e] * pre_w[e];
+        s[0] += u[e];
+        s[1] = fmaf(u[e], y[e], s[1]);
+        acc[kPreW][e] = fmaf(dz[e], y[e], acc[kPreW][e]);
+        acc[kPreB][e] += dz[e];
+      }
+      row_sums<NT, 2>(s, tmp, turn);
+      const float m0 = a.pre == HTTM_NORM_LAYER ? s[0] * inv_c : 0.f, m1 = s[1] * inv_c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = fmaf(r, u[e] - m0 - y[e] * m1, g[e]);
+    }
+    if (a.dx) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = a.rs * g[e];
+      cols.store(static_cast<TX*>(a.dx) + row * a.sdx, 0, o);
+    }
+    if (a.f) {
+      if (a.post == HTTM_NORM_NONE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          acc[kGate][e] = fmaf(g[e], f[e], acc[kGate][e]);
+          g[e] *= gate[e];
+        }
+      } else {
+        const float mean = a.post == HTTM_NORM_LAYER ? a.stats[row] : 0.f, r = a.stats[a.rows + row];
+        float s[2] = {0.f, 0.f}, u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[e] = cols.live(0, e) ? (f[e] - mean) * r : 0.f;
+          acc[kGate][e] = fmaf(g[e], fmaf(f[e], post_w[e], post_b[e]), acc[kGate][e]);
+          g[e] *= gate[e];
+          acc[kPostW][e] = fmaf(g[e], f[e], acc[kPostW][e]);
+          acc[kPostB][e] += g[e];
+          u[e] = g[e] * post_w[e];
+          s[0] += u[e];
+          s[1] = fmaf(u[e], f[e], s[1]);
+        }
+        row_sums<NT, 2>(s, tmp, turn);
+        const float m0 = a.post == HTTM_NORM_LAYER ? s[0] * inv_c : 0.f, m1 = s[1] * inv_c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = r * (u[e] - m0 - f[e] * m1);
+      }
+      if (a.df) cols.store(static_cast<TF*>(a.df) + row * a.sdf, 0, g);
+    }
+  }
+  const int64_t n_part = (int64_t)n_gates * a.chunks;
+#pragma unroll
+  for (int k = 0; k < kNumGrads; ++k)
+    if (a.want >> k & 1) cols.store(a.partial + ((int64_t)__popc(a.want & ((1u << k) - 1)) * n_part + group) * a.C, 0, acc[k]);
+}
+
+struct SumArgs {
+  const float* partial;
+  float* out[kNumGrads];     // wanted gradients, in the order of the partial sums
+  int is_gate0;              // out[0] is the gate's: summed per gate group
+  int C, gates, chunks;
+};
+
+// Adds up the partial rows: 32 channels a block, 32 threads down the rows,
+// each in order, then the 32 in order.
+__global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
+  __shared__ float s[32][33];
+  const int k = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x;
+  const bool per_gate = k == 0 && a.is_gate0;
+  const int64_t n_part = (int64_t)a.gates * a.chunks;
+  const int64_t p0 = per_gate ? (int64_t)blockIdx.z * a.chunks : 0, n = per_gate ? a.chunks : n_part;
+  if (!per_gate && blockIdx.z > 0) return;
+  float v = 0.f;
+  if (col < a.C) {
+    const float* p = a.partial + ((int64_t)k * n_part + p0) * a.C + col;
+#pragma unroll 4
+    for (int64_t i = threadIdx.y; i < n; i += 32) v += p[i * a.C];
+  }
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && col < a.C) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    a.out[k][(per_gate ? (int64_t)blockIdx.z * a.C : 0) + col] = t;
+  }
+}
+
+// Thread groups per gate group of the backward kernel: enough groups to
+// fill the SMs (about 512 threads each), at least 4 rows each.
+int grad_threads(int C) {
+  int nt = 32;
+  while (nt * 8 < C) nt *= 2;
+  return nt;
+}
+int grad_chunks(const httm_norm_cfg& c) {
+  const int64_t gates = std::max(1, c.gates), rows = c.rows / gates;
+  const int64_t want = std::max<int64_t>(1, (int64_t)kSMs * 512 / grad_threads(c.channels) / gates);
+  return (int)std::max<int64_t>(1, std::min(want, rows / 4));
+}
+
+template <class TX, class TF, bool VEC>
+cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
+#define HTTM_NORM_FWD(NT, V)                                                                        \
+  do {                                                                                              \
+    constexpr int kRows = (NT) > 32 ? 1 : 4;                                                        \
+    const int64_t grid = (a.rows + kRows - 1) / kRows;                                              \
+    gated_norm_kernel<TX, TF, NT, V, VEC><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a);     \
+  } while (0)
+  if (a.C <= 256) HTTM_NORM_FWD(32, 1);
+  else if (a.C <= 512) HTTM_NORM_FWD(32, 2);
+  else if (a.C <= 1024) HTTM_NORM_FWD(32, 4);
+  else if (a.C <= 2048) HTTM_NORM_FWD(128, 2);
+  else if (a.C <= 4096) HTTM_NORM_FWD(256, 2);
+  else HTTM_NORM_FWD(512, 2);
+#undef HTTM_NORM_FWD
+  return cudaGetLastError();
+}
+
+template <class TX, class TF, bool VEC>
+cudaError_t launch_grad(const NormArgs& a, cudaStream_t s) {
+#define HTTM_NORM_BWD(NT)                                                                          \
+  do {                                                                                             \
+    constexpr int kGroups = (NT) > 32 ? 1 : 4;                                                     \
+    const int64_t grid = ((int64_t)std::max(1, a.gates) * a.chunks + kGroups - 1) / kGroups;       \
+    gated_norm_grad_kernel<TX, TF, NT, VEC><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a);  \
+  } while (0)
+  switch (grad_threads(a.C)) {
+    case 32: HTTM_NORM_BWD(32); break;
+    case 64: HTTM_NORM_BWD(64); break;
+    case 128: HTTM_NORM_BWD(128); break;
+    case 256: HTTM_NORM_BWD(256); break;
+    case 512: HTTM_NORM_BWD(512); break;
+    default: HTTM_NORM_BWD(1024); break;
+  }
+#undef HTTM_NORM_BWD
+  return cudaGetLastError();
+}
+
+httm_status check_cfg(const httm_norm_cfg* c) {
+  if (!c) return HTTM_ERR_ARG;
+  auto dtype_ok = [](int t) { return t == HTTM_BF16 || t == HTTM_F32; };
+  if (c->rows < 0 || c->channels < 1 || c->gates < 0) return HTTM_ERR_ARG;
+  if (!dtype_ok(c->stream_dtype) || !dtype_ok(c->branch_dtype)) return HTTM_ERR_ARG;
+  for (int kind : {c->post, c->pre})
+    if (kind < HTTM_NORM_NONE || kind > HTTM_NORM_RMS) return HTTM_ERR_ARG;
+  if (c->gates > 0 && c->rows % c->gates != 0) return HTTM_ERR_ARG;
+  if (!(c->post_eps >= 0.f) || !(c->pre_eps >= 0.f)) return HTTM_ERR_ARG;
+  if (!(c->residual_scale - c->residual_scale == 0.f)) return HTTM_ERR_ARG;
+  if (c->channels > kMaxChannels || c->gates > kMaxGates || c->rows > 0x7fffffffll) return HTTM_ERR_UNSUPPORTED;
+  if (c->stream_dtype == HTTM_BF16 && c->branch_dtype == HTTM_F32) return HTTM_ERR_UNSUPPORTED;
+  return HTTM_OK;
+}
+
+size_t elem(int dtype) { return dtype == HTTM_F32 ? 4 : 2; }
+
+// A [rows, C] argument: present, aligned to its type, and (an output) with
+// rows that do not overlap.  Clears *wide when it needs element accesses.
+httm_status check_rows(const httm_rows* r, int64_t rows, int C, int dtype, bool output, bool* wide) {
+  if (!r->data) return HTTM_ERR_ARG;
+  if (!aligned(r->data, elem(dtype))) return HTTM_ERR_ALIGN;
+  if (output && rows > 1 && (r->row < 0 ? -r->row : r->row) < C) return HTTM_ERR_ARG;
+  if (!aligned(r->data, 16) || (rows > 1 && r->row % (int64_t)(16 / elem(dtype)) != 0)) *wide = false;
+  return HTTM_OK;
+}
+httm_status check_param(const float* p, bool* wide) {
+  if (!p) return HTTM_OK;
+  if (!aligned(p, 4)) return HTTM_ERR_ALIGN;
+  if (!aligned(p, 16)) *wide = false;
+  return HTTM_OK;
+}
+
+template <class Fn>
+cudaError_t by_type(const httm_norm_cfg& c, bool wide, Fn&& fn) {
+  using bf16 = __nv_bfloat16;
+  if (c.stream_dtype == HTTM_F32 && c.branch_dtype == HTTM_F32)
+    return wide ? fn(float{}, float{}, std::true_type{}) : fn(float{}, float{}, std::false_type{});
+  if (c.stream_dtype == HTTM_F32)
+    return wide ? fn(float{}, bf16{}, std::true_type{}) : fn(float{}, bf16{}, std::false_type{});
+  return wide ? fn(bf16{}, bf16{}, std::true_type{}) : fn(bf16{}, bf16{}, std::false_type{});
+}
+
+}  // namespace
+}  // namespace httm
+
+using namespace httm;
+
+#define HTTM_TRY(expr)                   \
+  do {                                   \
+    const httm_status t_ = (expr);       \
+    if (t_ != HTTM_OK) return t_;        \
+  } while (0)
+
+extern "C" {
+
+httm_status httm_gated_norm_forward(const httm_norm_cfg* c, const httm_norm_weights* w, const httm_rows* x,
+                                    const httm_rows* f, const httm_rows* y, const httm_rows* z, float* stats,
+                                    void* stream) {
+  HTTM_TRY(check_cfg(c));
+  if (!w || !x || (c->pre != HTTM_NORM_NONE) != (z != nullptr)) return HTTM_ERR_ARG;
+  if ((c->gates > 0) != (w->gate != nullptr)) return HTTM_ERR_ARG;
+  if (!f && (c->post != HTTM_NORM_NONE || c->gates > 0)) return HTTM_ERR_ARG;
+  if (!y && (f || c->residual_scale != 1.f || !z)) return HTTM_ERR_ARG;
+  if (c->rows == 0) return HTTM_OK;
+  bool wide = c->channels % 8 == 0;
+  NormArgs a{};
+  HTTM_TRY(check_rows(x, c->rows, c->channels, c->stream_dtype, false, &wide));
+  a.x = x->data, a.sx = x->row;
+  if (f) {
+    HTTM_TRY(check_rows(f, c->rows, c->channels, c->branch_dtype, false, &wide));
+    a.f = f->data, a.sf = f->row;
+  }
+  if (y) {
+    HTTM_TRY(check_rows(y, c->rows, c->channels, c->stream_dtype, true, &wide));
+    a.y_out = y->data, a.sy = y->row;
+  }
+  if (z) {
+    HTTM_TRY(check_rows(z, c->rows, c->channels, c->branch_dtype, true, &wide));
+    a.z = z->data, a.sz = z->row;
+  }
+  for (const float* p : {w->gate, w->post_weight, w->post_bias, w->pre_weight, w->pre_bias})
+    HTTM_TRY(check_param(p, &wide));
+  if (stats && !aligned(stats, 4)) return HTTM_ERR_ALIGN;
+  a.gate = w->gate;
+  a.post_w = w->post_weight, a.post_b = w->post_bias, a.pre_w = w->pre_weight, a.pre_b = w->pre_bias;
+  a.stats = stats;
+  a.rows = c->rows;
+  a.gates = c->gates;
+  a.gate_rows = c->rows / std::max(1, c->gates);
+  a.C = c->channels;
+  a.post = c->post, a.pre = c->pre;
+  a.post_eps = c->post_eps, a.pre_eps = c->pre_eps, a.rs = c->residual_scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto vec) {
+    return launch_forward<decltype(tx), decltype(tf), decltype(vec)::value>(a, s);
+  }), s);
+  return HTTM_OK;
+}
+
+httm_status httm_gated_norm_workspace_bytes(const httm_norm_cfg* c, size_t* bytes) {
+  HTTM_TRY(check_cfg(c));
+  if (!bytes) return HTTM_ERR_ARG;
+  *bytes = (size_t)kNumGrads * std::max(1, c->gates) * grad_chunks(*c) * c->channels * sizeof(float);
+  return HTTM_OK;
+}
+
+httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_weights* w, const httm_rows* dy,
+                                     const httm_rows* dz, const httm_rows* f, const httm_rows* y, const float* stats,
+                                     const httm_rows* dx, const httm_rows* df, const httm_norm_grads* grads,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  HTTM_TRY(check_cfg(c));
+  const bool pre = c->pre != HTTM_NORM_NONE, post = c->post != HTTM_NORM_NONE;
+  if (!w || !grads || pre != (dz != nullptr)) return HTTM_ERR_ARG;
+  if ((c->gates > 0) != (w->gate != nullptr)) return HTTM_ERR_ARG;
+  if (!f && (post || c->gates > 0 || df)) return HTTM_ERR_ARG;
+  if (pre && c->rows > 0 && !y) return HTTM_ERR_ARG;
+  if ((pre || post) && c->rows > 0 && !stats) return HTTM_ERR_ARG;
+  if ((grads->gate && !c->gates) || ((grads->post_weight || grads->post_bias) && !post) ||
+      ((grads->pre_weight || grads->pre_bias) && !pre))
+    return HTTM_ERR_ARG;
+  bool wide = c->channels % 8 == 0;
+  NormArgs a{};
+  if (c->rows > 0) {
+    if (dy) {
+      HTTM_TRY(check_rows(dy, c->rows, c->channels, c->stream_dtype, false, &wide));
+      a.dy = dy->data, a.sdy = dy->row;
+    }
+    if (dz) {
+      HTTM_TRY(check_rows(dz, c->rows, c->channels, c->branch_dtype, false, &wide));
+      a.dz = dz->data, a.sdz = dz->row;
+    }
+    if (f) {
+      HTTM_TRY(check_rows(f, c->rows, c->channels, c->branch_dtype, false, &wide));
+      a.f = f->data, a.sf = f->row;
+    }
+    if (pre) {
+      HTTM_TRY(check_rows(y, c->rows, c->channels, c->stream_dtype, false, &wide));
+      a.y = y->data, a.sy = y->row;
+    }
+    if (dx) {
+      HTTM_TRY(check_rows(dx, c->rows, c->channels, c->stream_dtype, true, &wide));
+      a.dx = dx->data, a.sdx = dx->row;
+    }
+    if (df) {
+      HTTM_TRY(check_rows(df, c->rows, c->channels, c->branch_dtype, true, &wide));
+      a.df = df->data, a.sdf = df->row;
+    }
+  }
+  for (const float* p : {w->gate, w->post_weight, w->post_bias, w->pre_weight, w->pre_bias})
+    HTTM_TRY(check_param(p, &wide));
+  bool any = true;
+  for (const float* p : {grads->gate, grads->post_weight, grads->post_bias, grads->pre_weight, grads->pre_bias})
+    HTTM_TRY(check_param(p, &any));
+  if (stats && !aligned(stats, 4)) return HTTM_ERR_ALIGN;
+  SumArgs sum{};
+  float* outs[kNumGrads] = {grads->gate, grads->post_weight, grads->post_bias, grads->pre_weight, grads->pre_bias};
+  int n_out = 0;
+  for (int k = 0; k < kNumGrads; ++k)
+    if (outs[k]) {
+      a.want |= 1u << k;
+      sum.out[n_out++] = outs[k];
+    }
+  a.chunks = grad_chunks(*c);
+  a.gates = std::max(1, c->gates);
+  const size_t need = (size_t)n_out * a.gates * a.chunks * c->channels * sizeof(float);
+  if (need && (!workspace || workspace_bytes < need)) return HTTM_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 256)) return HTTM_ERR_ALIGN;
+  a.partial = static_cast<float*>(workspace);
+  a.gate = w->gate;
+  a.post_w = w->post_weight, a.post_b = w->post_bias, a.pre_w = w->pre_weight, a.pre_b = w->pre_bias;
+  a.stats = const_cast<float*>(stats);
+  a.rows = c->rows;
+  a.gate_rows = c->rows / a.gates;
+  a.C = c->channels;
+  a.post = c->post, a.pre = c->pre;
+  a.rs = c->residual_scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c->rows == 0 && !n_out) return HTTM_OK;
+  HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto vec) {
+    return launch_grad<decltype(tx), decltype(tf), decltype(vec)::value>(a, s);
+  }), s);
+  if (n_out) {
+    sum.partial = a.partial;
+    sum.is_gate0 = grads->gate != nullptr;
+    sum.C = c->channels;
+    sum.gates = a.gates;
+    sum.chunks = a.chunks;
+    const dim3 grid((c->channels + 31) / 32, n_out, sum.is_gate0 ? a.gates : 1);
+    norm_sum_kernel<<<grid, dim3(32, 32), 0, s>>>(sum);
+    HTTM_OPS_LAUNCH(cudaGetLastError(), s);
+  }
+  return HTTM_OK;
+}
+
+}  // extern "C"

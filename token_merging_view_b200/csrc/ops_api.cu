@@ -1,0 +1,57 @@
+// The device state that the operators around the layer report through.
+#include <atomic>
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace httm {
+namespace {
+
+// One per device that loads the library: status 0, and the 2 s bound of
+// every device wait.
+__device__ DevState g_ops_state = {0, 0, 0, 0, {0, 0, 0, 0, 0, 0, 0, 0}, 0, 0, 0, 0, 0, 2000000000ull};
+
+}  // namespace
+
+DevState* ops_state() {
+  static std::atomic<DevState*> cached[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return nullptr;
+  if (dev < 64)
+    if (DevState* p = cached[dev].load(std::memory_order_acquire)) return p;
+  // looking an address up is no stream work: allowed while the calling
+  // thread captures a graph
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_ops_state);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return nullptr;
+  if (dev < 64) cached[dev].store(static_cast<DevState*>(p), std::memory_order_release);
+  return static_cast<DevState*>(p);
+}
+
+}  // namespace httm
+
+using namespace httm;
+
+extern "C" httm_status httm_ops_device_status(void* stream, uint32_t* status) {
+  if (!status) return HTTM_ERR_ARG;
+  *status = 0;
+  DevState* st = ops_state();
+  if (!st) return cuda_fail(cudaGetLastError(), "ops_state");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t bits = 0;
+  cudaError_t e = cudaMemcpyAsync(&bits, &st->status, sizeof(bits), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && bits) {
+    // the status word and the record of the first wait that ran out
+    e = cudaMemsetAsync(&st->status, 0, sizeof(uint32_t), s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(&st->wait_site, 0, 3 * sizeof(uint32_t), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "httm_ops_device_status");
+  *status = bits;
+  if (bits & HTTM_DEV_TIMEOUT) return HTTM_ERR_TIMEOUT;
+  return bits ? HTTM_ERR_DEVICE_BOUNDS : HTTM_OK;
+}

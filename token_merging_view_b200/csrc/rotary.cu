@@ -1,0 +1,260 @@
+// Rotary positions: pairs of channels turned by position * frequency, from
+// any strided layout into any other (a packed projection into [h, N, d]).
+//
+// The operator is bound by memory: every element is read and written once.
+// An angle belongs to (token, pair) and serves every head, so a thread owns
+// W pairs of one token, computes their cosines and sines once, and walks
+// over the heads of both tensors.  Four neighbouring threads of a 64-channel
+// head read and write whole 128-byte rows.  When there are few tokens the
+// heads are divided among more threads.
+//
+// Angles: frequencies are given in radians per position (fp64).  In turns
+// and 64-bit fixed point, position * frequency is one integer product whose
+// overflow drops whole turns exactly; what is left is the fp64 rounding of
+// the frequency itself (2^-53 of it, times the position) and 2^-33 turns
+// from keeping the top 32 bits.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace httm {
+namespace {
+
+struct RotaryArgs {
+  View in[2], out[2];           // queries, keys
+  int heads[2];
+  int batch, tokens, axes, pairs, d, rot;
+  int chunks, tail_chunks;      // W-pair chunks of a head, W-channel chunks of what is copied
+  int head_groups, heads_per;   // the heads divided among threads
+  const int32_t* pos;
+  int64_t pos_batch;
+  const double* freqs;
+  float factor;
+  int inverse;
+};
+
+// W consecutive elements as floats; W = 8 goes in 16-byte accesses.
+template <class T, int W>
+__device__ __forceinline__ void load_w(const T* p, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = to_f(*p);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(p)[i];
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    }
+  } else {
+    static_assert(W == 8, "bf16 vectors are 16 bytes");
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+template <class T, int W>
+__device__ __forceinline__ void store_w(T* p, const float (&v)[W]) {
+  if constexpr (W == 1) {
+    *p = from_f<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// cos and sin of pos * freq (freq in radians per position, any sign).
+__device__ __forceinline__ void turn(double freq, int pos, float factor, bool inverse, float& c, float& s) {
+  // turns per position as a 64-bit fraction of one turn (whole turns drop out)
+  const double t = freq * 0.15915494309189533577;            // 1 / (2 pi)
+  const double frac = t - floor(t);
+  const unsigned long long step = __double2ull_rn(frac * 18446744073709551616.0);   // 1.0 saturates to 2^64 - 1
+  const long long phase = (long long)(step * (unsigned long long)(long long)pos);
+  // the top 32 bits, in half turns: [-1, 1)
+  const float half = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;      // 2^-31
+  sincospif(half, &s, &c);
+  c *= factor;
+  s *= inverse ? -factor : factor;
+}
+
+// (a, b) turned: the products are contracted by hand, so that every path
+// gives the same bits.
+__device__ __forceinline__ void turn_pair(float a, float b, float c, float s, float& x, float& y) {
+  x = fmaf(a, c, -__fmul_rn(b, s));
+  y = fmaf(b, c, __fmul_rn(a, s));
+}
+
+template <class T, int W, bool HALF>
+__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a) {
+  const int per_token = a.chunks + a.tail_chunks;
+  const long long total = (long long)a.batch * a.head_groups * a.tokens * per_token;
+  const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (at >= total) return;
+  int ch, tok, hg, b;
+  if (total <= 0x7fffffffll) {             // 32-bit divisions where they do
+    uint32_t i = (uint32_t)at;
+    ch = i % (uint32_t)per_token, i /= (uint32_t)per_token;
+    tok = i % (uint32_t)a.tokens, i /= (uint32_t)a.tokens;
+    hg = i % (uint32_t)a.head_groups, b = i / (uint32_t)a.head_groups;
+  } else {
+    long long i = at;
+    ch = (int)(i % per_token), i /= per_token;
+    tok = (int)(i % a.tokens), i /= a.tokens;
+    hg = (int)(i % a.head_groups), b = (int)(i / a.head_groups);
+  }
+  const bool copied = ch >= a.chunks;
+
+  float c[W], s[W];
+  int lo, hi;                              // first channel of the two runs of W this thread handles
+  if (copied) {
+    lo = a.rot + (ch - a.chunks) * W;
+    hi = lo;
+  } else {
+    const int p0 = ch * W;                 // first pair, counted over all axes
+    if (HALF) {                            // W divides the pairs of an axis: one axis per chunk
+      const int ax = p0 / a.pairs, n = p0 - ax * a.pairs;
+      lo = ax * 2 * a.pairs + n;
+      hi = lo + a.pairs;
+    } else {
+      lo = 2 * p0;
+      hi = lo + W;
+    }
+    const int32_t* pos = a.pos + b * a.pos_batch + (long long)tok * a.axes;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int ax = (p0 + e) / a.pairs, n = p0 + e - ax * a.pairs;
+      turn(a.freqs[n], pos[ax], a.factor, a.inverse != 0, c[e], s[e]);
+    }
+  }
+
+  const int h0 = hg * a.heads_per, h1 = min(h0 + a.heads_per, a.heads[0] + a.heads[1]);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const int which = h >= a.heads[0] ? 1 : 0, hh = which ? h - a.heads[0] : h;
+    const View &vi = a.in[which], &vo = a.out[which];
+    const T* x = reinterpret_cast<const T*>(vi.data) + b * vi.sb + hh * vi.sh + tok * vi.st;
+    T* y = reinterpret_cast<T*>(vo.data) + b * vo.sb + hh * vo.sh + tok * vo.st;
+    float u[W], v[W];
+    load_w<T, W>(x + lo, u);
+    if (copied) {
+      store_w<T, W>(y + lo, u);
+      continue;
+    }
+    load_w<T, W>(x + hi, v);
+    float p[W], q[W];
+    if constexpr (HALF || W == 1) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) turn_pair(u[e], v[e], c[e], s[e], p[e], q[e]);
+    } else {                               // pairs lie side by side in the 2 W channels (u, v)
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e) {
+        turn_pair(u[2 * e], u[2 * e + 1], c[e], s[e], p[2 * e], p[2 * e + 1]);
+        turn_pair(v[2 * e], v[2 * e + 1], c[e + W / 2], s[e + W / 2], q[2 * e], q[2 * e + 1]);
+      }
+    }
+    store_w<T, W>(y + lo, p);
+    store_w<T, W>(y + hi, q);
+  }
+}
+
+template <class T, int W>
+cudaError_t launch_w(RotaryArgs& a, bool half, cudaStream_t s) {
+  a.chunks = a.axes * a.pairs / W;
+  a.tail_chunks = (a.d - a.rot) / W;
+  const long long work = (long long)a.batch * a.tokens * (a.chunks + a.tail_chunks);
+  const int heads = a.heads[0] + a.heads[1];
+  // a thread per (token, chunk) walks over all heads once there are enough
+  // of them for the loads in flight that the memory needs (about 1,024
+  // threads an SM); with fewer tokens the heads are divided
+  const long long want = (long long)kSMs * 1024;
+  a.head_groups = (int)std::min<long long>(heads, std::max<long long>(1, (want + work - 1) / work));
+  a.heads_per = (heads + a.head_groups - 1) / a.head_groups;
+  a.head_groups = (heads + a.heads_per - 1) / a.heads_per;
+  const int threads = work * a.head_groups < kSMs * 256 ? 64 : 256;
+  const long long grid = (work * a.head_groups + threads - 1) / threads;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  if (half)
+    rotary_kernel<T, W, true><<<(unsigned)grid, threads, 0, s>>>(a);
+  else
+    rotary_kernel<T, W, false><<<(unsigned)grid, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_t(RotaryArgs& a, bool half, cudaStream_t s) {
+  // 8 channels at a time where every run is a multiple of 8 and every row
+  // starts on 16 bytes; else one pair at a time
+  const int el = 16 / (int)sizeof(T);
+  bool wide = a.d % 8 == 0 && a.rot % 16 == 0 && (half ? a.pairs % 8 == 0 : true);
+  for (int w = 0; w < (a.heads[1] ? 2 : 1); ++w)
+    for (const View* v : {&a.in[w], &a.out[w]})
+      wide = wide && aligned(v->data, 16) && v->sb % el == 0 && v->sh % el == 0 && v->st % el == 0;
+  return wide ? launch_w<T, 8>(a, half, s) : launch_w<T, 1>(a, half, s);
+}
+
+}  // namespace
+}  // namespace httm
+
+using namespace httm;
+
+extern "C" httm_status httm_rotary(const httm_rotary_cfg* c, const httm_view* q, const httm_view* q_out,
+                                   const httm_view* k, const httm_view* k_out, void* stream) {
+  if (!c || !q || !q_out) return HTTM_ERR_ARG;
+  if (c->batch < 0 || c->tokens < 0 || c->heads < 1 || c->kv_heads < 0) return HTTM_ERR_ARG;
+  if (c->d_head < 1 || c->axes < 1 || c->axes > 4 || c->pairs < 1) return HTTM_ERR_ARG;
+  if (2ll * c->axes * c->pairs > c->d_head) return HTTM_ERR_ARG;
+  if (c->layout != HTTM_ROTARY_HALF && c->layout != HTTM_ROTARY_PAIRS) return HTTM_ERR_ARG;
+  if (c->dtype != HTTM_BF16 && c->dtype != HTTM_F32) return HTTM_ERR_ARG;
+  if (c->position_batch < 0 || !(c->factor - c->factor == 0.f)) return HTTM_ERR_ARG;
+  if (c->d_head > 1024) return HTTM_ERR_UNSUPPORTED;
+  if ((long long)c->heads + c->kv_heads > (1 << 20)) return HTTM_ERR_UNSUPPORTED;
+  if (c->kv_heads > 0 && (!k || !k_out)) return HTTM_ERR_ARG;
+  if (c->batch == 0 || c->tokens == 0) return HTTM_OK;
+  if (!c->positions || !c->freqs) return HTTM_ERR_ARG;
+  if (!aligned(c->positions, 4) || !aligned(c->freqs, 8)) return HTTM_ERR_ALIGN;
+  const size_t es = c->dtype == HTTM_F32 ? 4 : 2;
+  RotaryArgs a{};
+  const int heads[2] = {c->heads, c->kv_heads};
+  const httm_view* in[2] = {q, k};
+  const httm_view* out[2] = {q_out, k_out};
+  for (int w = 0; w < 2; ++w) {
+    a.heads[w] = heads[w];
+    if (heads[w] == 0) continue;
+    for (const httm_view* v : {in[w], out[w]}) {
+      if (!v->data || v->batch < 0 || v->head < 0 || v->token < 0) return HTTM_ERR_ARG;
+      if (!aligned(v->data, es)) return HTTM_ERR_ALIGN;
+    }
+    a.in[w] = normal_view(*in[w], c->batch, heads[w], c->tokens);
+    a.out[w] = normal_view(*out[w], c->batch, heads[w], c->tokens);
+    if (!disjoint(a.out[w], c->batch, heads[w], c->tokens, c->d_head)) return HTTM_ERR_ARG;
+  }
+  a.batch = c->batch;
+  a.tokens = c->tokens;
+  a.axes = c->axes;
+  a.pairs = c->pairs;
+  a.d = c->d_head;
+  a.rot = 2 * c->axes * c->pairs;
+  a.pos = c->positions;
+  a.pos_batch = c->position_batch;
+  a.freqs = c->freqs;
+  a.factor = c->factor;
+  a.inverse = c->inverse;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = c->layout == HTTM_ROTARY_HALF;
+  HTTM_OPS_LAUNCH(c->dtype == HTTM_F32 ? launch_t<float>(a, half, s) : launch_t<__nv_bfloat16>(a, half, s), s);
+  return HTTM_OK;
+}
