@@ -3,10 +3,10 @@
 //   dV = P^T dO,  dP = dO V^T,  dS = P o (dP - D),  dQ = c dS K,  dK = c dS^T Q.
 //
 // Three launches (a fourth when key tiles are split):
-//  - attn_prep_kernel: D and lse * log2(e) of every query row, padded to
+//  - attn_prep_kernel: -D and -lse * log2(e) of every query row, padded to
 //    whole tiles (rows outside the sequence or with an empty range get
-//    lse = +inf, so their P is 0 without a compare), and the key ranges of
-//    rows and of query tiles;
+//    -infinity for the latter, so their P is 0 without a compare), and the
+//    key ranges of rows and of query tiles;
 //  - attn_dkv_kernel: a CTA owns 128 keys and walks over the query tiles
 //    that see them, for all query heads sharing the key head; dK and dV stay
 //    in TMEM.  Everything is transposed (rows = keys): S^T = K Q^T and dP^T
@@ -50,7 +50,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ------------------------------------------------------------------ prep
 // 128 rows of one head a block, 8 threads a row.
 __global__ void __launch_bounds__(256)
-attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restrict__ lse2, float* __restrict__ dsum,
+attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restrict__ nlse, float* __restrict__ ndsum,
                  int2* __restrict__ ranges, AttnTileRange* __restrict__ tiles) {
   __shared__ AttnTileRange part[8];
   const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, c = threadIdx.x & 7;
@@ -77,8 +77,8 @@ attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restr
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (c == 0) {
-      lse2[bh * Lp + l] = live ? a.lse_in[(size_t)bh * a.L + l] * kLog2e : INFINITY;
-      dsum[bh * Lp + l] = s;
+      nlse[bh * Lp + l] = live ? a.lse_in[(size_t)bh * a.L + l] * -kLog2e : -INFINITY;
+      ndsum[bh * Lp + l] = -s;
       if (h == 0) ranges[b * Lp + l] = keys;
     }
     if (live) {
@@ -131,15 +131,30 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, const uint8_t* 
     umma_bf16_ts(d, a_col(A, kk), sw128_desc(y + kk * 16 * 128, 1024), id, (add || kk > 0) ? 1u : 0u);
 }
 
+// Two neighbouring scores: s -> 2^(s c + m).
+__device__ __forceinline__ void exp2_pair(uint32_t& s0, uint32_t& s1, unsigned long long cc, unsigned long long m) {
+  float x0, x1;
+  f2_unpack(f2_fma(f2_pack(__uint_as_float(s0), __uint_as_float(s1)), cc, m), x0, x1);
+  s0 = __float_as_uint(ex2(x0));
+  s1 = __float_as_uint(ex2(x1));
+}
+// Two neighbouring p (dP + nd), packed to bf16.
+__device__ __forceinline__ uint32_t ds_pair(uint32_t p0, uint32_t p1, uint32_t g0, uint32_t g1, unsigned long long nd) {
+  float x0, x1;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(p0), __uint_as_float(p1)),
+                   f2_add(f2_pack(__uint_as_float(g0), __uint_as_float(g1)), nd)), x0, x1);
+  return pack_bf16(x0, x1);
+}
+
 // ------------------------------------------------------------------ dK, dV
 struct DkvSmem {
   uint8_t k[kTileBytes], v[kTileBytes];
   uint8_t q[kStages][kTileBytes], g[kStages][kTileBytes];     // query and dout tiles
-  float lse2[kStages][kAttnTile], dsum[kStages][kAttnTile];
+  float nlse[kStages][kAttnTile], ndsum[kStages][kAttnTile];
   int2 range[kStages][kAttnTile];
   uint32_t active[kMaxQTiles / 32], masked[kMaxQTiles / 32], dead[kMaxQTiles / 32];
   uint64_t kv_full, q_full[kStages], q_empty[kStages];
-  uint64_t full[3], p_ready[2], ds_ready[2], drain;
+  uint64_t full[3], p_ready[2], ds_ready[2], drain, dirty, clean;
   int count[kThreads / 32];
   uint32_t tmem_base;
   int abort;
@@ -184,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
                 const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
                 const __grid_constant__ AttnArgs a, int q_tiles, int k_tiles, int parts,
-                const float* __restrict__ lse2, const float* __restrict__ dsum, const int2* __restrict__ ranges,
+                const float* __restrict__ nlse, const float* __restrict__ ndsum, const int2* __restrict__ ranges,
                 const AttnTileRange* __restrict__ tiles, float* __restrict__ part_out) {
   extern __shared__ uint8_t smem_raw[];
   DkvSmem& sm = *reinterpret_cast<DkvSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -230,6 +245,8 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       mbar_init(&sm.ds_ready[i], 256);
     }
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.dirty, 1);
+    mbar_init(&sm.clean, 1);
     sm.abort = 0;
     mbar_fence_init();
   }
@@ -260,64 +277,64 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         mbar_arrive_expect_tx(&sm.q_full[s], 2 * kTileBytes + kAttnTile * 16);
         tma_load_tile(sm.q[s], mq, &sm.q_full[s], t * kAttnTile, h, b);
         tma_load_tile(sm.g[s], mg, &sm.q_full[s], t * kAttnTile, h, b);
-        bulk_load(sm.lse2[s], lse2 + at, kAttnTile * 4, &sm.q_full[s]);
-        bulk_load(sm.dsum[s], dsum + at, kAttnTile * 4, &sm.q_full[s]);
+        bulk_load(sm.nlse[s], nlse + at, kAttnTile * 4, &sm.q_full[s]);
+        bulk_load(sm.ndsum[s], ndsum + at, kAttnTile * 4, &sm.q_full[s]);
         bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kAttnTile, kAttnTile * 8, &sm.q_full[s]);
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ MMA issue
-      bool ok = n > 0 && __all_sync(0xffffffffu, mbar_wait(&sm.kv_full, 0, abort, st));
       TileWalk walk(sm.active, words, n_active, s0);
+      int n_dirty = 0;
       auto issue_s = [&](int i) -> bool {                       // S_i: product 2 i
         const int s = i % kStages, t = walk.next();
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st))) return false;
+        if (!mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) return false;
         if (sm.dead[t >> 5] >> (t & 31) & 1) {                  // rows that may hold anything
-          zero_rows(sm.q[s], [&](int r) { return sm.lse2[s][r] == INFINITY; });
-          zero_rows(sm.g[s], [&](int r) { return sm.lse2[s][r] == INFINITY; });
-          fence_async_smem();
-          __syncwarp();
+          mbar_arrive(&sm.dirty);
+          if (!mbar_wait(&sm.clean, n_dirty++ & 1, abort, st)) return false;
         }
-        if (lane == 0) {
-          tc_fence_after();
-          const int buf = (2 * i) % 3;
-          mma_rows(tmem + buf * 128, sm.k, sm.q[s]);
-          umma_commit(&sm.full[buf]);
-        }
-        __syncwarp();
+        tc_fence_after();
+        mma_rows(tmem + ((2 * i) % 3) * 128, sm.k, sm.q[s]);
+        umma_commit(&sm.full[(2 * i) % 3]);
         return true;
       };
       auto issue_dp = [&](int i) {                              // dP_i: product 2 i + 1
-        if (lane == 0) {
-          const int buf = (2 * i + 1) % 3;
-          mma_rows(tmem + buf * 128, sm.v, sm.g[i % kStages]);
-          umma_commit(&sm.full[buf]);
-        }
-        __syncwarp();
+        mma_rows(tmem + ((2 * i + 1) % 3) * 128, sm.v, sm.g[i % kStages]);
+        umma_commit(&sm.full[(2 * i + 1) % 3]);
       };
+      bool ok = mbar_wait(&sm.kv_full, 0, abort, st);
       if (ok) ok = issue_s(0);
       if (ok) issue_dp(0);
       if (ok && n > 1) ok = issue_s(1);
       for (int i = 0; ok && i < n; ++i) {
         const int s = i % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.p_ready[i & 1], (i >> 1) & 1, abort, st))) break;
-        if (lane == 0) {
-          tc_fence_after();
-          mma_cols(tmem + kColA, tmem + ((2 * i) % 3) * 128, sm.g[s], i > 0);
-        }
-        __syncwarp();
+        if (!mbar_wait(&sm.p_ready[i & 1], (i >> 1) & 1, abort, st)) break;
+        tc_fence_after();
+        mma_cols(tmem + kColA, tmem + ((2 * i) % 3) * 128, sm.g[s], i > 0);
         if (i + 1 < n) issue_dp(i + 1);                         // into the buffer dV_i reads from
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.ds_ready[i & 1], (i >> 1) & 1, abort, st))) break;
-        if (lane == 0) {
-          tc_fence_after();
-          mma_cols(tmem + kColB, tmem + ((2 * i + 1) % 3) * 128, sm.q[s], i > 0);
-          umma_commit(&sm.q_empty[s]);
-        }
-        __syncwarp();
+        if (!mbar_wait(&sm.ds_ready[i & 1], (i >> 1) & 1, abort, st)) break;
+        tc_fence_after();
+        mma_cols(tmem + kColB, tmem + ((2 * i + 1) % 3) * 128, sm.q[s], i > 0);
+        umma_commit(&sm.q_empty[s]);
         if (i + 2 < n) ok = issue_s(i + 2);                     // into the buffer dK_i reads from
       }
-      if (lane == 0) {
-        umma_commit(&sm.drain);
-        drain_mma(&sm.drain, 0);
+      umma_commit(&sm.drain);
+      drain_mma(&sm.drain, 0);
+    } else if (warp == 2 && n > 0) {
+      // ------------------------------------------------------------ rows that see nothing
+      TileWalk walk(sm.active, words, n_active, s0);
+      int n_dirty = 0;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % kStages, t = walk.next();
+        if (!(sm.dead[t >> 5] >> (t & 31) & 1)) continue;
+        // the issuing thread says when the stage is there, and waits
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.dirty, n_dirty++ & 1, abort, st)) ||
+            !__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)))
+          break;
+        zero_rows(sm.q[s], [&](int r) { return sm.nlse[s][r] == -INFINITY; });
+        zero_rows(sm.g[s], [&](int r) { return sm.nlse[s][r] == -INFINITY; });
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.clean);
       }
     }
   } else {
@@ -326,7 +343,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
     const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int key = k0 + row;
-    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), neg = f2_pack(-1.f, -1.f);
+    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2);
     bool ok = true;
     if (n > 0) {
       TileWalk walk(sm.active, words, n_active, s0);
@@ -341,19 +358,15 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
           break;
         }
         tc_fence_after();
-        uint32_t p[64];
-        tmem_ld64(ts, p);
         // p = 2^(s c - lse2) of this key and the 64 queries of the columns
-        const float4* lp = reinterpret_cast<const float4*>(sm.lse2[s] + wg * 64);
-        uint32_t pk[32];
+        uint32_t p[64], pk[32];
+        tmem_ld64(ts, p);
+        const ulonglong2* lp = reinterpret_cast<const ulonglong2*>(sm.nlse[s] + wg * 64);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float4 m = lp[e];
-          float x[4];
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(p[4 * e]), __uint_as_float(p[4 * e + 1])), cc, f2_mul(f2_pack(m.x, m.y), neg)), x[0], x[1]);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(p[4 * e + 2]), __uint_as_float(p[4 * e + 3])), cc, f2_mul(f2_pack(m.z, m.w), neg)), x[2], x[3]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) p[4 * e + c] = __float_as_uint(ex2(x[c]));
+          const ulonglong2 m = lp[e];
+          exp2_pair(p[4 * e], p[4 * e + 1], cc, m.x);
+          exp2_pair(p[4 * e + 2], p[4 * e + 3], cc, m.y);
         }
         if (masked) {
           const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + wg * 64);
@@ -378,21 +391,18 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         tc_fence_after();
         uint32_t g[64];
         tmem_ld64(td, g);
-        const float4* dp = reinterpret_cast<const float4*>(sm.dsum[s] + wg * 64);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (p[e] == 0u) g[e] = 0u;                          // a value nobody sees may be NaN
+        }
+        const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(sm.ndsum[s] + wg * 64);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float4 m = dp[e];
-          const float ms[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float pv = __uint_as_float(p[4 * e + c]);
-            float ds = pv * (__uint_as_float(g[4 * e + c]) - ms[c]);
-            if (masked && pv == 0.f) ds = 0.f;                  // a value nobody sees may be NaN
-            g[4 * e + c] = __float_as_uint(ds);
-          }
+          const ulonglong2 m = dp[e];
+          pk[2 * e] = ds_pair(p[4 * e], p[4 * e + 1], g[4 * e], g[4 * e + 1], m.x);
+          pk[2 * e + 1] = ds_pair(p[4 * e + 2], p[4 * e + 3], g[4 * e + 2], g[4 * e + 3], m.y);
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
         tmem_st32(td, pk);
         tmem_wait_st();
         tc_fence_before();
@@ -466,7 +476,7 @@ struct DqSmem {
   uint8_t q[kTileBytes], g[kTileBytes];
   uint8_t k[kStages][kTileBytes], v[kStages][kTileBytes];
   uint64_t q_full, kv_full[kStages], kv_empty[kStages];
-  uint64_t full[3], s_read[2], ds_ready[2], drain;
+  uint64_t full[3], s_read[2], ds_ready[2], drain, dirty, clean;
   uint32_t tmem_base;
   int abort;
 };
@@ -476,8 +486,8 @@ static_assert(kDqSmem <= 227 * 1024, "shared memory");
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
                const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
-               const __grid_constant__ AttnArgs a, int q_tiles, const float* __restrict__ lse2,
-               const float* __restrict__ dsum, const int2* __restrict__ ranges,
+               const __grid_constant__ AttnArgs a, int q_tiles, const float* __restrict__ nlse,
+               const float* __restrict__ ndsum, const int2* __restrict__ ranges,
                const AttnTileRange* __restrict__ tiles) {
   extern __shared__ uint8_t smem_raw[];
   DqSmem& sm = *reinterpret_cast<DqSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -487,6 +497,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
   const size_t Lp = (size_t)q_tiles * kAttnTile;
   const AttnTileRange tr = tiles[(size_t)b * q_tiles + qt];
   const int n = tr.lo < tr.hi ? (tr.hi - tr.lo + kAttnTile - 1) / kAttnTile : 0, base = n > 0 ? tr.lo : 0;
+  const int n_last = tr.hi - (base + (n - 1) * kAttnTile);     // keys of the union in the last tile
   DevState* st = a.st;
 
   if (threadIdx.x == 0) {
@@ -501,6 +512,8 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       mbar_init(&sm.ds_ready[i], 256);
     }
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.dirty, 1);
+    mbar_init(&sm.clean, 1);
     sm.abort = 0;
     mbar_fence_init();
   }
@@ -525,54 +538,49 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
         tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kAttnTile, kh, b);
         tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kAttnTile, kh, b);
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ MMA issue
-      bool ok = n > 0 && __all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, abort, st));
       auto issue_s = [&](int j) -> bool {
         const int s = j % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st))) return false;
-        const int n_valid = tr.hi - (base + j * kAttnTile);
-        if (n_valid < kAttnTile) {                              // K rows behind the union of the ranges
-          zero_rows(sm.k[s], [&](int r) { return r >= n_valid; });
-          fence_async_smem();
-          __syncwarp();
+        if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
+        if (j == n - 1 && n_last < kAttnTile) {
+          mbar_arrive(&sm.dirty);
+          if (!mbar_wait(&sm.clean, 0, abort, st)) return false;
         }
-        if (lane == 0) {
-          tc_fence_after();
-          const int buf = (2 * j) % 3;
-          mma_rows(tmem + buf * 128, sm.q, sm.k[s]);
-          umma_commit(&sm.full[buf]);
-        }
-        __syncwarp();
+        tc_fence_after();
+        mma_rows(tmem + ((2 * j) % 3) * 128, sm.q, sm.k[s]);
+        umma_commit(&sm.full[(2 * j) % 3]);
         return true;
       };
       auto issue_dp = [&](int j) {
-        if (lane == 0) {
-          const int buf = (2 * j + 1) % 3;
-          mma_rows(tmem + buf * 128, sm.g, sm.v[j % kStages]);
-          umma_commit(&sm.full[buf]);
-        }
-        __syncwarp();
+        mma_rows(tmem + ((2 * j + 1) % 3) * 128, sm.g, sm.v[j % kStages]);
+        umma_commit(&sm.full[(2 * j + 1) % 3]);
       };
+      bool ok = mbar_wait(&sm.q_full, 0, abort, st);
       if (ok) ok = issue_s(0);
       if (ok) issue_dp(0);
       if (ok && n > 1) ok = issue_s(1);
       for (int j = 0; ok && j < n; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_read[j & 1], (j >> 1) & 1, abort, st))) break;
+        if (!mbar_wait(&sm.s_read[j & 1], (j >> 1) & 1, abort, st)) break;
         tc_fence_after();
         if (j + 1 < n) issue_dp(j + 1);                         // into the buffer S_j was read from
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.ds_ready[j & 1], (j >> 1) & 1, abort, st))) break;
-        if (lane == 0) {
-          tc_fence_after();
-          mma_cols(tmem + kColA, tmem + ((2 * j + 1) % 3) * 128, sm.k[j % kStages], j > 0);
-          umma_commit(&sm.kv_empty[j % kStages]);
-        }
-        __syncwarp();
+        if (!mbar_wait(&sm.ds_ready[j & 1], (j >> 1) & 1, abort, st)) break;
+        tc_fence_after();
+        mma_cols(tmem + kColA, tmem + ((2 * j + 1) % 3) * 128, sm.k[j % kStages], j > 0);
+        umma_commit(&sm.kv_empty[j % kStages]);
         if (j + 2 < n) ok = issue_s(j + 2);                     // into the buffer dQ_j reads from
       }
-      if (lane == 0) {
-        umma_commit(&sm.drain);
-        drain_mma(&sm.drain, 0);
+      umma_commit(&sm.drain);
+      drain_mma(&sm.drain, 0);
+    } else if (warp == 2 && n > 0 && n_last < kAttnTile) {
+      // ------------------------------------------------------------ K rows behind the union of the ranges
+      const int s = (n - 1) % kStages;
+      if (__all_sync(0xffffffffu, mbar_wait(&sm.dirty, 0, abort, st)) &&
+          __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n - 1) / kStages) & 1, abort, st))) {
+        zero_rows(sm.k[s], [&](int r) { return r >= n_last; });
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.clean);
       }
     }
   } else {
@@ -581,10 +589,12 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
     const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int l = qt * kAttnTile + row;                         // below Lp
-    const float m = lse2[(size_t)bh * Lp + l], D = dsum[(size_t)bh * Lp + l];
+    const float m = nlse[(size_t)bh * Lp + l], nd = ndsum[(size_t)bh * Lp + l];
     const int2 keys = ranges[b * Lp + l];
     const bool live = keys.x < keys.y;
-    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), mm = f2_pack(-m, -m);
+    const int f_lo = warp_max(live ? keys.x : 0) - base - wg * 64;   // every live row of the warp sees [f_lo, f_hi)
+    const int f_hi = warp_min(live ? keys.y : 0x7fffffff) - base - wg * 64;
+    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), mm = f2_pack(m, m), dd = f2_pack(nd, nd);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint32_t ts = tmem + lane_off + ((2 * j) % 3) * 128 + wg * 64;
@@ -595,16 +605,11 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       tmem_ld64(ts, p);
       tc_fence_before();
       mbar_arrive(&sm.s_read[j & 1]);
-      const int first = keys.x - (base + j * kAttnTile) - wg * 64, last = keys.y - (base + j * kAttnTile) - wg * 64;
-      const bool masked = __any_sync(0xffffffffu, first > 0 || last < 64);
+      const bool masked = f_lo > j * kAttnTile || f_hi < j * kAttnTile + 64;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        float x0, x1;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1])), cc, mm), x0, x1);
-        p[2 * e] = __float_as_uint(ex2(x0));
-        p[2 * e + 1] = __float_as_uint(ex2(x1));
-      }
+      for (int e = 0; e < 32; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc, mm);
       if (masked) {
+        const int first = keys.x - base - wg * 64 - j * kAttnTile, last = keys.y - base - wg * 64 - j * kAttnTile;
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e < first || e >= last) p[e] = 0u;
@@ -613,15 +618,13 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       tc_fence_after();
       uint32_t g[64], pk[32];
       tmem_ld64(td, g);
+      if (masked) {
 #pragma unroll
-      for (int e = 0; e < 64; ++e) {
-        const float pv = __uint_as_float(p[e]);
-        float ds = pv * (__uint_as_float(g[e]) - D);
-        if (masked && pv == 0.f) ds = 0.f;                      // a value nobody sees may be NaN
-        g[e] = __float_as_uint(ds);
+        for (int e = 0; e < 64; ++e)
+          if (p[e] == 0u) g[e] = 0u;                            // a value nobody sees may be NaN
       }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+      for (int e = 0; e < 32; ++e) pk[e] = ds_pair(p[2 * e], p[2 * e + 1], g[2 * e], g[2 * e + 1], dd);
       tmem_st32(td, pk);
       tmem_wait_st();
       tc_fence_before();
@@ -694,8 +697,8 @@ AttnBwdPlan attn_bwd_plan(const httm_attention& a) {
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, cudaStream_t s) {
   char* w = static_cast<char*>(ws);
-  float* lse2 = reinterpret_cast<float*>(w + p.stat);
-  float* dsum = lse2 + (size_t)a.B * a.H * p.Lp;
+  float* nlse = reinterpret_cast<float*>(w + p.stat);
+  float* ndsum = nlse + (size_t)a.B * a.H * p.Lp;
   int2* ranges = reinterpret_cast<int2*>(w + p.range);
   AttnTileRange* tiles = reinterpret_cast<AttnTileRange*>(w + p.tiles);
   float* part = reinterpret_cast<float*>(w + p.part);
@@ -710,13 +713,13 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, c
       (e = cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem)) != cudaSuccess)
     return e;
   if (p.q_tiles > 0) {
-    attn_prep_kernel<<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, lse2, dsum, ranges, tiles);
+    attn_prep_kernel<<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, nlse, ndsum, ranges, tiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (p.k_tiles > 0) {
     const long long items = (long long)a.B * a.K * p.k_tiles;
     attn_dkv_kernel<<<(unsigned)(items * p.kv_parts), kThreads, kDkvSmem, s>>>(
-        mq, mg, mk, mv, a, p.q_tiles, p.k_tiles, p.kv_parts, lse2, dsum, ranges, tiles, part);
+        mq, mg, mk, mv, a, p.q_tiles, p.k_tiles, p.kv_parts, nlse, ndsum, ranges, tiles, part);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.kv_parts > 1) {
       const long long rows = 2ll * a.B * a.K * a.N;
@@ -726,7 +729,7 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, c
   }
   if (p.q_tiles > 0)
     attn_dq_kernel<<<(unsigned)((long long)a.B * a.H * p.q_tiles), kThreads, kDqSmem, s>>>(mq, mg, mk, mv, a, p.q_tiles,
-                                                                                         lse2, dsum, ranges, tiles);
+                                                                                         nlse, ndsum, ranges, tiles);
   return cudaGetLastError();
 }
 

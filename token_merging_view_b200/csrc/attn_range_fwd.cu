@@ -50,7 +50,7 @@ struct FwdSmem {
   uint64_t q_full;
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t s_full[3], p_full[2], o_done[2];
-  uint64_t drain;
+  uint64_t drain, dirty, clean;
   int lo[8], hi[8];
   uint32_t tmem_base;
   int abort;
@@ -100,6 +100,8 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       mbar_init(&sm.o_done[i], 1);
     }
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.dirty, 1);
+    mbar_init(&sm.clean, 1);
     sm.abort = 0;
     mbar_fence_init();
   }
@@ -120,6 +122,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
   const int j0 = (int)((long long)n_all * part / parts);
   const int n_kv = (int)((long long)n_all * (part + 1) / parts) - j0;
   const int base = n_all > 0 ? lo + j0 * kAttnTile : 0;
+  const int n_last = hi - (base + (n_kv - 1) * kAttnTile);   // keys of the union in the last tile
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
@@ -132,55 +135,54 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
         tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kAttnTile, kh, b);
         tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kAttnTile, kh, b);
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 && lane == 0 && n_kv > 0) {
       // ------------------------------------------------------------ MMA issue
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_o = idesc_bf16(128, kAttnD, false, true);
       const int n_prod = n_t * n_kv;                 // S products: i = n_t j + tile
-      bool ok = n_kv > 0 && __all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, abort, st));
       // product i: waits for its K/V tile if it is the tile's first
       auto issue_qk = [&](int i) -> bool {
         const int j = n_t == 2 ? i >> 1 : i, tile = n_t == 2 ? i & 1 : 0, s = j % kStages;
         if (tile == 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st))) return false;
-          const int n_valid = hi - (base + j * kAttnTile);
-          if (n_valid < kAttnTile) {                 // V rows behind the union of the ranges
-            zero_rows(sm.v[s], [&](int r) { return r >= n_valid; });
-            fence_async_smem();
-            __syncwarp();
+          if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
+          if (j == n_kv - 1 && n_last < kAttnTile) {
+            mbar_arrive(&sm.dirty);
+            if (!mbar_wait(&sm.clean, 0, abort, st)) return false;
           }
-        }
-        if (lane == 0) {
           tc_fence_after();
-          const uint32_t qa = smem_u32(sm.q[tile]), ka = smem_u32(sm.k[s]), col = tmem + (i % 3) * 128;
-#pragma unroll
-          for (int kk = 0; kk < kAttnD / 16; ++kk)
-            umma_bf16(col, sw128_desc(qa + kk * 32, 1024), sw128_desc(ka + kk * 32, 1024), id_s, kk > 0);
-          umma_commit(&sm.s_full[i % 3]);
         }
-        __syncwarp();
+        const uint32_t qa = smem_u32(sm.q[tile]), ka = smem_u32(sm.k[s]), col = tmem + (i % 3) * 128;
+#pragma unroll
+        for (int kk = 0; kk < kAttnD / 16; ++kk)
+          umma_bf16(col, sw128_desc(qa + kk * 32, 1024), sw128_desc(ka + kk * 32, 1024), id_s, kk > 0);
+        umma_commit(&sm.s_full[i % 3]);
         return true;
       };
+      bool ok = mbar_wait(&sm.q_full, 0, abort, st);
       for (int i = 0; ok && i < min(3, n_prod); ++i) ok = issue_qk(i);
       for (int i = 0; ok && i < n_prod; ++i) {
         const int j = n_t == 2 ? i >> 1 : i, tile = n_t == 2 ? i & 1 : 0, s = j % kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_full[tile], j & 1, abort, st));
-        if (!ok) break;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint32_t va = smem_u32(sm.v[s]), pc = tmem + (i % 3) * 128, oc = tmem + kColO + tile * 64;
+        if (!mbar_wait(&sm.p_full[tile], j & 1, abort, st)) break;
+        tc_fence_after();
+        const uint32_t va = smem_u32(sm.v[s]), pc = tmem + (i % 3) * 128, oc = tmem + kColO + tile * 64;
 #pragma unroll
-          for (int kk = 0; kk < kAttnTile / 16; ++kk)
-            umma_bf16_ts(oc, pc + kk * 8, sw128_desc(va + kk * 16 * 128, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&sm.o_done[tile]);
-          if (tile == n_t - 1) umma_commit(&sm.kv_empty[s]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < kAttnTile / 16; ++kk)
+          umma_bf16_ts(oc, pc + kk * 8, sw128_desc(va + kk * 16 * 128, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&sm.o_done[tile]);
+        if (tile == n_t - 1) umma_commit(&sm.kv_empty[s]);
         if (i + 3 < n_prod) ok = issue_qk(i + 3);
       }
-      if (lane == 0) {                               // every MMA ends before TMEM is released
-        umma_commit(&sm.drain);
-        drain_mma(&sm.drain, 0);
+      umma_commit(&sm.drain);                        // every MMA ends before TMEM is released
+      drain_mma(&sm.drain, 0);
+    } else if (warp == 2 && n_kv > 0 && n_last < kAttnTile) {
+      // ------------------------------------------------------------ V rows behind the union of the ranges
+      const int s = (n_kv - 1) % kStages;
+      if (__all_sync(0xffffffffu, mbar_wait(&sm.dirty, 0, abort, st)) &&
+          __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n_kv - 1) / kStages) & 1, abort, st))) {
+        zero_rows(sm.v[s], [&](int r) { return r >= n_last; });
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.clean);
       }
     }
   } else {
@@ -191,6 +193,9 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       const uint32_t to = tmem + lane_off + kColO + t * 64;      // this row of O_t
       const bool live = keys.x < keys.y;
       const bool warp_live = __any_sync(0xffffffffu, live);
+      // the warp's keys: some row sees [w_lo, w_hi), every live row [f_lo, f_hi)
+      const int w_lo = warp_min(live ? keys.x : 0x7fffffff) - base, w_hi = warp_max(live ? keys.y : 0) - base;
+      const int f_lo = warp_max(live ? keys.x : 0) - base, f_hi = warp_min(live ? keys.y : 0x7fffffff) - base;
       // the row's queries into the swizzled tile (zeros behind d, and for
       // rows that see nothing, whatever memory holds there)
       {
@@ -214,10 +219,9 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
         // waits are made warp-uniform: tcgen05.ld/st below need every lane
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[buf], (i / 3) & 1, abort, st))) { ok = false; break; }
         tc_fence_after();
-        const int first = keys.x - (base + j * kAttnTile), last = keys.y - (base + j * kAttnTile);
+        const int k0 = j * kAttnTile;                            // the tile's keys, counted from base
         bool pv_done = j == 0;                                   // PV(t, j-1) seen complete
-        const bool sees = live && first < kAttnTile && last > 0;
-        if (!__any_sync(0xffffffffu, sees)) {
+        if (w_lo >= k0 + kAttnTile || w_hi <= k0) {
           // none of this warp's rows sees this tile: P = 0 (rows that are
           // never stored may keep what is there)
           if (warp_live) {
@@ -232,7 +236,8 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           tmem_wait_ld();
-          if (__any_sync(0xffffffffu, first > 0 || last < kAttnTile)) {
+          if (f_lo > k0 || f_hi < k0 + kAttnTile) {
+            const int first = keys.x - base - k0, last = keys.y - base - k0;
 #pragma unroll
             for (int e = 0; e < kAttnTile; ++e)
               if (e < first || e >= last) sr[e] = __float_as_uint(-INFINITY);
