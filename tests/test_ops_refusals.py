@@ -91,10 +91,9 @@ def test_attention_workspace_is_a_function_of_the_sizes():
     f, b = ops.httm_attention_workspace_bytes(1, 16, 16, 1, 1369, 64)
     assert f > 0 and f % 4 == 0
     assert ops.httm_attention_workspace_bytes(0, 16, 16, 1, 1369, 64) == (0, 0)
-    # lse and D of every padded query row, the ranges of rows and of tiles
+    # at least lse and D of every query row and head, and every row's range
     b = ops.httm_attention_workspace_bytes(30, 16, 16, 1369, 1369, 64)[1]
-    rows = 11 * 128
-    assert b == 30 * 16 * rows * 8 + 30 * rows * 8 + -(-30 * 11 * 32 // 256) * 256
+    assert 30 * 1369 * (16 * 8 + 8) <= b <= 30 * 1536 * (16 * 8 + 8) + 30 * 16 * 32 + 1024
 
 
 def _rot(**kw):

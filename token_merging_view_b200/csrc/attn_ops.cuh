@@ -34,10 +34,10 @@ __device__ __forceinline__ int2 key_range(const AttnArgs& a, int b, int l) {
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
-// A full warp: zero the rows r of a swizzled tile for which dead(r) holds.
+// A full warp: zero the rows r < n of a swizzled tile for which dead(r) holds.
 template <class F>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, F&& dead) {
-  for (int r = threadIdx.x & 31; r < kAttnTile; r += 32)
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int n, F&& dead) {
+  for (int r = threadIdx.x & 31; r < n; r += 32)
     if (dead(r)) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(tile + r * 128)[c] = make_uint4(0, 0, 0, 0);

@@ -7,6 +7,7 @@
 namespace httm {
 
 constexpr int kAttnTile = 128;          // keys, or query rows, of one tensor-core tile
+constexpr int kAttnStep = 96;           // queries (dK, dV) or keys (dQ) of one step of the backward kernels
 constexpr int kAttnD = 64;              // channels of a tile; narrower heads are padded with zeros
 constexpr int kAttnMaxQ = 1 << 21;      // queries of one sequence
 constexpr int kAttnMaxParts = 64;       // key splits of one forward work item
@@ -23,7 +24,7 @@ struct AttnArgs {
 };
 
 // The 4-D tensor map (channels, tokens, heads, batch) of a bf16 view, boxes
-// of 128 tokens x 64 channels with 128-byte swizzle; what lies behind the
+// of `box` tokens x 64 channels with 128-byte swizzle; what lies behind the
 // last token or channel reads as zero.  A broadcast dimension (stride 0) has
 // extent 1 in the map: its coordinate is multiplied by 0.  `spare`: the base
 // address where the view has none (no tokens: nothing is loaded through it).
@@ -31,7 +32,7 @@ struct AttnMap {
   CUtensorMap map;
   int hmul, bmul;
 };
-bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch);
+bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch, int box);
 
 // Forward: work items of up to 256 query rows, each in `parts` key ranges.
 struct AttnFwdPlan {
@@ -52,7 +53,7 @@ struct AttnTileRange {
   int pad[3];
 };
 struct AttnBwdPlan {
-  int q_tiles, k_tiles, Lp;             // Lp = q_tiles * 128
+  int q_tiles, k_tiles, Lp;             // tiles of kAttnStep queries, of 128 keys; Lp: rows kept per head
   int kv_parts;                         // splits of the queries of one key tile
   size_t stat, range, tiles, part, total;
 };

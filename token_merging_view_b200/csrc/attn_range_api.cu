@@ -76,7 +76,7 @@ AttnArgs base_args(const httm_attention& a) {
 
 }  // namespace
 
-bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch) {
+bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch, int rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   m->hmul = heads > 1 && v.sh > 0 ? 1 : 0;
@@ -87,7 +87,7 @@ bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, i
                               (cuuint64_t)(m->bmul ? batch : 1)};
   const cuuint64_t strides[3] = {tokens > 1 ? (cuuint64_t)v.st * 2 : row, m->hmul ? (cuuint64_t)v.sh * 2 : row,
                                  m->bmul ? (cuuint64_t)v.sb * 2 : row};
-  const cuuint32_t box[4] = {(cuuint32_t)kAttnD, (cuuint32_t)kAttnTile, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)kAttnD, (cuuint32_t)rows, 1, 1};
   const cuuint32_t step[4] = {1, 1, 1, 1};
   return enc(&m->map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -19,19 +19,22 @@
 // key-owning CTAs needs either atomics, whose order would change the result
 // from run to run, or N x N / 128 partial sums.
 //
-// Both kernels: warp 0 loads (TMA), warp 1 issues tcgen05.mma, warps 4..11
-// compute -- all eight on the same tile, warpgroup w on its columns [64 w,
-// 64 w + 64), TMEM lane = row.  Products alternate S_0 dP_0 S_1 dP_1 ...
-// through a ring of three 128-column TMEM buffers; P or dS overwrites its
-// own warpgroup's columns of the product it came from (32 columns of bf16
-// pairs at 0 and at 64).  While dS_i is computed the tensor core does the
-// products that P_i freed, and the other way round.
+// Both kernels move in steps of 96 (queries, or keys for dQ): two groups of
+// warps take the even and the odd steps, each with its own S and dP in TMEM
+// (2 x 2 x 96 columns; the accumulators take the other 128), so that one
+// group exponentiates while the other forms dS, and neither waits for a
+// buffer of the other.  P overwrites its S and dS its dP, as bf16 pairs.
+// Warp 0 loads (TMA), warp 1 issues the products S and dP, warp 3 those that
+// P and dS enter: one thread issues an N = 64 product at half the tensor
+// core's rate, two keep it fed; each accumulator has one issuing thread, so
+// its order of summation is fixed.  Warp 2 clears loaded rows that may hold
+// anything.  A group is kHalves warpgroups of 4 warps (TMEM lane = row),
+// each with 96 / kHalves of the columns.
 //
-// Parity waits: p_ready / s_read and ds_ready are two barriers each, used
-// by even and odd steps: step i + 2 cannot be reached by any warp before
-// the issuing warp has seen step i (its products are issued behind that
-// wait), so no barrier is ever two phases from a wait on it and none gets
-// an arrival of a later step early.
+// Parity waits: a barrier of a group completes one phase per step of that
+// group, and no phase can begin before every waiter has seen the one before:
+// S of the group's next step is issued behind the product that read P (or
+// the reads of S), dP behind the product that read dS.
 #include <algorithm>
 
 #include "attn_ops.cuh"
@@ -42,23 +45,31 @@ namespace {
 using namespace tc;
 
 constexpr int kStages = 4;
-constexpr int kThreads = 384;
-constexpr int kMaxQTiles = kAttnMaxQ / kAttnTile;
+constexpr int kStep = kAttnStep;
+constexpr int kHalves = 2;                            // warpgroups of a group
+constexpr int kCols = kStep / kHalves;                // columns of a thread
+constexpr int kChunk = 16;                            // columns in registers at a time
+constexpr int kGroupThreads = kHalves * 128;
+constexpr int kThreads = 128 + 2 * kGroupThreads;
+constexpr uint32_t kStepBytes = kStep * kAttnD * 2;   // 12 KB
+constexpr int kMaxQTiles = (kAttnMaxQ + kStep - 1) / kStep;
+constexpr int kMaxWords = (kMaxQTiles + 31) / 32;
 constexpr uint32_t kColA = 384, kColB = 448;          // accumulators (dV, dK; dQ in kColA)
 constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kCols % kChunk == 0 && kCols % 16 == 0, "whole chunks, whole K steps");
 
 // ------------------------------------------------------------------ prep
-// 128 rows of one head a block, 8 threads a row.
+// One step's 96 rows of one head a block, 8 threads a row.
 __global__ void __launch_bounds__(256)
 attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restrict__ nlse, float* __restrict__ ndsum,
                  int2* __restrict__ ranges, AttnTileRange* __restrict__ tiles) {
   __shared__ AttnTileRange part[8];
   const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, c = threadIdx.x & 7;
-  const size_t Lp = (size_t)q_tiles * kAttnTile;
+  const size_t Lp = (size_t)q_tiles * kStep;
   AttnTileRange tr{0x7fffffff, 0, 0, 0x7fffffff, 0, {0, 0, 0}};
 #pragma unroll
-  for (int pass = 0; pass < 4; ++pass) {
-    const int l = blockIdx.x * kAttnTile + pass * 32 + (threadIdx.x >> 3);
+  for (int pass = 0; pass < kStep / 32; ++pass) {
+    const int l = blockIdx.x * kStep + pass * 32 + (threadIdx.x >> 3);
     const int2 keys = l < a.L ? key_range(a, b, l) : make_int2(0, 0);
     const bool live = keys.x < keys.y;
     float s = 0.f;
@@ -110,25 +121,25 @@ attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restr
   }
 }
 
-// The A operand of K step kk (16 of the 128 columns) of a P or dS that the
-// two warpgroups wrote into their halves of buffer `col`.
-__device__ __forceinline__ uint32_t a_col(uint32_t col, int kk) { return col + (kk >> 2) * 64 + (kk & 3) * 8; }
-
-// D (+)= A B^T, both K-major tiles of 128 rows x 64 channels.
+// D = A B^T: K-major tiles of 128 and of 96 rows x 64 channels.
 __device__ __forceinline__ void mma_rows(uint32_t d, const uint8_t* A, const uint8_t* B) {
-  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t id = idesc_bf16(128, kStep, false, false);
   const uint32_t x = smem_u32(A), y = smem_u32(B);
 #pragma unroll
   for (int kk = 0; kk < kAttnD / 16; ++kk)
     umma_bf16(d, sw128_desc(x + kk * 32, 1024), sw128_desc(y + kk * 32, 1024), id, kk > 0);
 }
-// D (+)= A B, A in TMEM (128 x 128), B a tile of 128 rows x 64 channels.
+// D (+)= A B: A the 128 x 96 P or dS that the warpgroups of a group wrote to
+// the front of their columns of the product at `A`; B a tile of 96 rows x 64
+// channels.
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, const uint8_t* B, bool add) {
   constexpr uint32_t id = idesc_bf16(128, kAttnD, false, true);
+  constexpr int per = kCols / 16;                     // K steps of one warpgroup's columns
   const uint32_t y = smem_u32(B);
 #pragma unroll
-  for (int kk = 0; kk < kAttnTile / 16; ++kk)
-    umma_bf16_ts(d, a_col(A, kk), sw128_desc(y + kk * 16 * 128, 1024), id, (add || kk > 0) ? 1u : 0u);
+  for (int kk = 0; kk < kStep / 16; ++kk)
+    umma_bf16_ts(d, A + (kk / per) * kCols + (kk % per) * 8, sw128_desc(y + kk * 16 * 128, 1024), id,
+                 (add || kk > 0) ? 1u : 0u);
 }
 
 // Two neighbouring scores: s -> 2^(s c + m).
@@ -149,18 +160,19 @@ __device__ __forceinline__ uint32_t ds_pair(uint32_t p0, uint32_t p1, uint32_t g
 // ------------------------------------------------------------------ dK, dV
 struct DkvSmem {
   uint8_t k[kTileBytes], v[kTileBytes];
-  uint8_t q[kStages][kTileBytes], g[kStages][kTileBytes];     // query and dout tiles
-  float nlse[kStages][kAttnTile], ndsum[kStages][kAttnTile];
-  int2 range[kStages][kAttnTile];
-  uint32_t active[kMaxQTiles / 32], masked[kMaxQTiles / 32], dead[kMaxQTiles / 32];
+  uint8_t q[kStages][kStepBytes], g[kStages][kStepBytes];     // query and dout tiles
+  float nlse[kStages][kStep], ndsum[kStages][kStep];
+  int2 range[kStages][kStep];
+  uint32_t active[kMaxWords], masked[kMaxWords], dead[kMaxWords];
   uint64_t kv_full, q_full[kStages], q_empty[kStages];
-  uint64_t full[3], p_ready[2], ds_ready[2], drain, dirty, clean;
+  uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2], p_used[2], ds_used[2], drain, dirty, clean;
   int count[kThreads / 32];
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kDkvSmem = sizeof(DkvSmem) + 1024;
 static_assert(kDkvSmem <= 227 * 1024, "shared memory");
+static_assert(kStepBytes % 1024 == 0, "tiles start on 1024 bytes");
 
 // Walks over the set bits of `active`, round after round (one per head).
 struct TileWalk {
@@ -208,7 +220,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
   const int bk = item / k_tiles, kt = item % k_tiles, b = bk / a.K, kh = bk % a.K;
   const int k0 = kt * kAttnTile, k1 = min(k0 + kAttnTile, a.N);
   const int words = (q_tiles + 31) / 32;
-  const size_t Lp = (size_t)q_tiles * kAttnTile;
+  const size_t Lp = (size_t)q_tiles * kStep;
   DevState* st = a.st;
 
   // which query tiles see these keys, which of them need compares, which
@@ -239,12 +251,15 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
     }
-    for (int i = 0; i < 3; ++i) mbar_init(&sm.full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.p_ready[i], 256);
-      mbar_init(&sm.ds_ready[i], 256);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.dp_full[i], 1);
+      mbar_init(&sm.p_ready[i], kGroupThreads);
+      mbar_init(&sm.ds_ready[i], kGroupThreads);
+      mbar_init(&sm.p_used[i], 1);
+      mbar_init(&sm.ds_used[i], 1);
     }
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain, 2);
     mbar_init(&sm.dirty, 1);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
@@ -263,7 +278,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
   const int s0 = (int)(all * part / parts), n = (int)(all * (part + 1) / parts) - s0;   // steps of this CTA
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
     if (warp == 0 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ producer
       mbar_arrive_expect_tx(&sm.kv_full, 2 * kTileBytes);
@@ -273,49 +288,50 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       for (int i = 0; i < n; ++i) {
         const int s = i % kStages, t = walk.next(), h = kh * a.G + walk.head;
         if (i >= kStages && !mbar_wait(&sm.q_empty[s], ((i / kStages) - 1) & 1, abort, st)) break;
-        const size_t at = ((size_t)b * a.H + h) * Lp + (size_t)t * kAttnTile;
-        mbar_arrive_expect_tx(&sm.q_full[s], 2 * kTileBytes + kAttnTile * 16);
-        tma_load_tile(sm.q[s], mq, &sm.q_full[s], t * kAttnTile, h, b);
-        tma_load_tile(sm.g[s], mg, &sm.q_full[s], t * kAttnTile, h, b);
-        bulk_load(sm.nlse[s], nlse + at, kAttnTile * 4, &sm.q_full[s]);
-        bulk_load(sm.ndsum[s], ndsum + at, kAttnTile * 4, &sm.q_full[s]);
-        bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kAttnTile, kAttnTile * 8, &sm.q_full[s]);
+        const size_t at = ((size_t)b * a.H + h) * Lp + (size_t)t * kStep;
+        mbar_arrive_expect_tx(&sm.q_full[s], 2 * kStepBytes + kStep * 16);
+        tma_load_tile(sm.q[s], mq, &sm.q_full[s], t * kStep, h, b);
+        tma_load_tile(sm.g[s], mg, &sm.q_full[s], t * kStep, h, b);
+        bulk_load(sm.nlse[s], nlse + at, kStep * 4, &sm.q_full[s]);
+        bulk_load(sm.ndsum[s], ndsum + at, kStep * 4, &sm.q_full[s]);
+        bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kStep, kStep * 8, &sm.q_full[s]);
       }
     } else if (warp == 1 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ MMA issue
+      // ------------------------------------------------------------ S^T and dP^T
       TileWalk walk(sm.active, words, n_active, s0);
       int n_dirty = 0;
-      auto issue_s = [&](int i) -> bool {                       // S_i: product 2 i
-        const int s = i % kStages, t = walk.next();
-        if (!mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) return false;
+      bool ok = mbar_wait(&sm.kv_full, 0, abort, st);
+      for (int i = 0; ok && i < n; ++i) {
+        const int s = i % kStages, t = walk.next(), grp = i & 1, m = i >> 1;
+        if (!mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) break;
         if (sm.dead[t >> 5] >> (t & 31) & 1) {                  // rows that may hold anything
           mbar_arrive(&sm.dirty);
-          if (!mbar_wait(&sm.clean, n_dirty++ & 1, abort, st)) return false;
+          if (!mbar_wait(&sm.clean, n_dirty++ & 1, abort, st)) break;
         }
+        if (m > 0 && !mbar_wait(&sm.p_used[grp], (m - 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_rows(tmem + ((2 * i) % 3) * 128, sm.k, sm.q[s]);
-        umma_commit(&sm.full[(2 * i) % 3]);
-        return true;
-      };
-      auto issue_dp = [&](int i) {                              // dP_i: product 2 i + 1
-        mma_rows(tmem + ((2 * i + 1) % 3) * 128, sm.v, sm.g[i % kStages]);
-        umma_commit(&sm.full[(2 * i + 1) % 3]);
-      };
-      bool ok = mbar_wait(&sm.kv_full, 0, abort, st);
-      if (ok) ok = issue_s(0);
-      if (ok) issue_dp(0);
-      if (ok && n > 1) ok = issue_s(1);
-      for (int i = 0; ok && i < n; ++i) {
-        const int s = i % kStages;
-        if (!mbar_wait(&sm.p_ready[i & 1], (i >> 1) & 1, abort, st)) break;
+        mma_rows(tmem + grp * 2 * kStep, sm.k, sm.q[s]);
+        umma_commit(&sm.s_full[grp]);
+        if (m > 0 && !mbar_wait(&sm.ds_used[grp], (m - 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_cols(tmem + kColA, tmem + ((2 * i) % 3) * 128, sm.g[s], i > 0);
-        if (i + 1 < n) issue_dp(i + 1);                         // into the buffer dV_i reads from
-        if (!mbar_wait(&sm.ds_ready[i & 1], (i >> 1) & 1, abort, st)) break;
+        mma_rows(tmem + grp * 2 * kStep + kStep, sm.v, sm.g[s]);
+        umma_commit(&sm.dp_full[grp]);
+      }
+      umma_commit(&sm.drain);
+      drain_mma(&sm.drain, 0);
+    } else if (warp == 3 && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ dV += P^T dO, dK += dS^T Q
+      for (int i = 0; i < n; ++i) {
+        const int s = i % kStages, grp = i & 1, m = i >> 1;
+        if (!mbar_wait(&sm.p_ready[grp], m & 1, abort, st)) break;
         tc_fence_after();
-        mma_cols(tmem + kColB, tmem + ((2 * i + 1) % 3) * 128, sm.q[s], i > 0);
+        mma_cols(tmem + kColA, tmem + grp * 2 * kStep, sm.g[s], i > 0);
+        umma_commit(&sm.p_used[grp]);
+        if (!mbar_wait(&sm.ds_ready[grp], m & 1, abort, st)) break;
+        tc_fence_after();
+        mma_cols(tmem + kColB, tmem + grp * 2 * kStep + kStep, sm.q[s], i > 0);
+        umma_commit(&sm.ds_used[grp]);
         umma_commit(&sm.q_empty[s]);
-        if (i + 2 < n) ok = issue_s(i + 2);                     // into the buffer dK_i reads from
       }
       umma_commit(&sm.drain);
       drain_mma(&sm.drain, 0);
@@ -330,107 +346,124 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.dirty, n_dirty++ & 1, abort, st)) ||
             !__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)))
           break;
-        zero_rows(sm.q[s], [&](int r) { return sm.nlse[s][r] == -INFINITY; });
-        zero_rows(sm.g[s], [&](int r) { return sm.nlse[s][r] == -INFINITY; });
+        zero_rows(sm.q[s], kStep, [&](int r) { return sm.nlse[s][r] == -INFINITY; });
+        zero_rows(sm.g[s], kStep, [&](int r) { return sm.nlse[s][r] == -INFINITY; });
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.clean);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
     // ------------------------------------------------------------ P and dS
-    const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const int grp = (warp - 4) / (4 * kHalves), half = ((warp - 4) >> 2) % kHalves, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + grp * 2 * kStep + half * kCols, td = ts + kStep;
     const int key = k0 + row;
     const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2);
     bool ok = true;
-    if (n > 0) {
+    if (n > grp) {
       TileWalk walk(sm.active, words, n_active, s0);
-      for (int i = 0; i < n; ++i) {
-        const int s = i % kStages, t = walk.next();
+      if (grp) walk.next();
+      for (int i = grp; i < n; i += 2) {
+        const int s = i % kStages, t = walk.next(), m = i >> 1;
         const bool masked = sm.masked[t >> 5] >> (t & 31) & 1;
-        const uint32_t ts = tmem + lane_off + ((2 * i) % 3) * 128 + wg * 64;
-        const uint32_t td = tmem + lane_off + ((2 * i + 1) % 3) * 128 + wg * 64;
+        if (i + 2 < n) walk.next();                             // the other group's
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) ||
-            !__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * i) % 3], ((2 * i) / 3) & 1, abort, st))) {
+            !__all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], m & 1, abort, st))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // p = 2^(s c - lse2) of this key and the 64 queries of the columns
-        uint32_t p[64], pk[32];
-        tmem_ld64(ts, p);
-        const ulonglong2* lp = reinterpret_cast<const ulonglong2*>(sm.nlse[s] + wg * 64);
+        // p = 2^(s c - lse2) of this key and the queries of the columns
+        uint32_t p[kCols];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const ulonglong2 m = lp[e];
-          exp2_pair(p[4 * e], p[4 * e + 1], cc, m.x);
-          exp2_pair(p[4 * e + 2], p[4 * e + 3], cc, m.y);
+        for (int c = 0; c < kCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
+        tmem_wait_ld();
+        const ulonglong2* lp = reinterpret_cast<const ulonglong2*>(sm.nlse[s] + half * kCols);
+#pragma unroll
+        for (int e = 0; e < kCols / 4; ++e) {
+          const ulonglong2 x = lp[e];
+          exp2_pair(p[4 * e], p[4 * e + 1], cc, x.x);
+          exp2_pair(p[4 * e + 2], p[4 * e + 3], cc, x.y);
         }
         if (masked) {
-          const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + wg * 64);
+          const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + half * kCols);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < kCols / 2; ++e) {
             const int4 r = rp[e];
             if (key < r.x || key >= r.y) p[2 * e] = 0u;
             if (key < r.z || key >= r.w) p[2 * e + 1] = 0u;
           }
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]));
-        tmem_st32(ts, pk);
+        for (int c = 0; c < kCols; c += kChunk) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            pk[e] = pack_bf16(__uint_as_float(p[c + 2 * e]), __uint_as_float(p[c + 2 * e + 1]));
+          tmem_st8(ts + c / 2, pk);
+        }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sm.p_ready[i & 1]);
+        mbar_arrive(&sm.p_ready[grp]);
         // dS = P (dP - D)
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * i + 1) % 3], ((2 * i + 1) / 3) & 1, abort, st))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.dp_full[grp], m & 1, abort, st))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t g[64];
-        tmem_ld64(td, g);
-        if (masked) {
+        const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(sm.ndsum[s] + half * kCols);
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (p[e] == 0u) g[e] = 0u;                          // a value nobody sees may be NaN
-        }
-        const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(sm.ndsum[s] + wg * 64);
+        for (int c = 0; c < kCols; c += kChunk) {
+          uint32_t g[16], pk[8];
+          tmem_ld16(td + c, g);
+          tmem_wait_ld();
+          if (masked) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const ulonglong2 m = dp[e];
-          pk[2 * e] = ds_pair(p[4 * e], p[4 * e + 1], g[4 * e], g[4 * e + 1], m.x);
-          pk[2 * e + 1] = ds_pair(p[4 * e + 2], p[4 * e + 3], g[4 * e + 2], g[4 * e + 3], m.y);
+            for (int e = 0; e < 16; ++e)
+              if (p[c + e] == 0u) g[e] = 0u;                    // a value nobody sees may be NaN
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const ulonglong2 x = dp[c / 4 + e];
+            pk[2 * e] = ds_pair(p[c + 4 * e], p[c + 4 * e + 1], g[4 * e], g[4 * e + 1], x.x);
+            pk[2 * e + 1] = ds_pair(p[c + 4 * e + 2], p[c + 4 * e + 3], g[4 * e + 2], g[4 * e + 3], x.y);
+          }
+          tmem_st8(td + c / 2, pk);
         }
-        tmem_st32(td, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sm.ds_ready[i & 1]);
+        mbar_arrive(&sm.ds_ready[grp]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
     }
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
     tc_fence_after();
-    // warpgroup 0 stores dV, warpgroup 1 dK
+    // the first group stores dV, the second dK; each warpgroup its channels
     if (ok) {
-      uint32_t o[64];
+      constexpr int kOut = kAttnD / kHalves;
+      uint32_t o[kOut];
       if (n > 0) {
-        tmem_ld64(tmem + lane_off + (wg == 0 ? kColA : kColB), o);
+#pragma unroll
+        for (int c = 0; c < kOut; c += 16)
+          tmem_ld16(tmem + lane_off + (grp == 0 ? kColA : kColB) + half * kOut + c, *reinterpret_cast<uint32_t(*)[16]>(&o[c]));
+        tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) o[e] = 0u;
+        for (int e = 0; e < kOut; ++e) o[e] = 0u;
       }
       if (parts > 1) {
-        float4* dst = reinterpret_cast<float4*>(part_out + (((size_t)blockIdx.x * 2 + wg) * kAttnTile + row) * kAttnD);
+        float4* dst = reinterpret_cast<float4*>(part_out + (((size_t)blockIdx.x * 2 + grp) * kAttnTile + row) * kAttnD +
+                                                half * kOut);
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
+        for (int v = 0; v < kOut / 4; ++v)
           dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]), __uint_as_float(o[4 * v + 2]),
                                __uint_as_float(o[4 * v + 3]));
       } else if (key < a.N) {
-        const View& w = wg == 0 ? a.dv : a.dk;
+        const View& w = grp == 0 ? a.dv : a.dk;
         __nv_bfloat16* dst =
             reinterpret_cast<__nv_bfloat16*>(w.data) + b * w.sb + kh * w.sh + (int64_t)key * w.st;
-        store_row_bf16<8>(o, dst, wg == 0 ? 1.f : a.scale, 0, a.d);
+        store_row_bf16<kOut / 8>(o, dst, grp == 0 ? 1.f : a.scale, half * kOut, a.d);
       }
     }
   }
@@ -474,9 +507,10 @@ attn_dkv_join_kernel(const __grid_constant__ AttnArgs a, int k_tiles, int parts,
 // ------------------------------------------------------------------ dQ
 struct DqSmem {
   uint8_t q[kTileBytes], g[kTileBytes];
-  uint8_t k[kStages][kTileBytes], v[kStages][kTileBytes];
+  uint8_t k[kStages][kStepBytes], v[kStages][kStepBytes];
   uint64_t q_full, kv_full[kStages], kv_empty[kStages];
-  uint64_t full[3], s_read[2], ds_ready[2], drain, dirty, clean;
+  uint64_t s_full[2], dp_full[2], s_read[2], ds_ready[2], ds_used[2], drain, dirty, clean;
+  int lo[4], hi[4];
   uint32_t tmem_base;
   int abort;
 };
@@ -487,17 +521,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
                const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
                const __grid_constant__ AttnArgs a, int q_tiles, const float* __restrict__ nlse,
-               const float* __restrict__ ndsum, const int2* __restrict__ ranges,
-               const AttnTileRange* __restrict__ tiles) {
+               const float* __restrict__ ndsum, const int2* __restrict__ ranges) {
   extern __shared__ uint8_t smem_raw[];
   DqSmem& sm = *reinterpret_cast<DqSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.x / q_tiles, qt = q_tiles - 1 - blockIdx.x % q_tiles;
+  const int m_tiles = (a.L + kAttnTile - 1) / kAttnTile;        // tiles of 128 queries; later ones first
+  const int bh = blockIdx.x / m_tiles, qt = m_tiles - 1 - blockIdx.x % m_tiles;
   const int b = bh / a.H, h = bh % a.H, kh = h / a.G;
-  const size_t Lp = (size_t)q_tiles * kAttnTile;
-  const AttnTileRange tr = tiles[(size_t)b * q_tiles + qt];
-  const int n = tr.lo < tr.hi ? (tr.hi - tr.lo + kAttnTile - 1) / kAttnTile : 0, base = n > 0 ? tr.lo : 0;
-  const int n_last = tr.hi - (base + (n - 1) * kAttnTile);     // keys of the union in the last tile
+  const size_t Lp = (size_t)q_tiles * kStep;
+  // this thread's query and its keys; the union of the tile's
+  const int half = ((warp - 4) >> 2) % kHalves, grp = (warp - 4) / (4 * kHalves);
+  const int row = (warp & 3) * 32 + lane, l = qt * kAttnTile + row;
+  const int2 keys = warp >= 4 && l < a.L ? ranges[b * Lp + l] : make_int2(0, 0);
+  const bool live = keys.x < keys.y;
+  if (warp >= 4 && warp < 8) {
+    const int x = warp_min(live ? keys.x : 0x7fffffff), y = warp_max(live ? keys.y : 0);
+    if (lane == 0) {
+      sm.lo[warp - 4] = x;
+      sm.hi[warp - 4] = y;
+    }
+  }
   DevState* st = a.st;
 
   if (threadIdx.x == 0) {
@@ -506,12 +549,14 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
-    for (int i = 0; i < 3; ++i) mbar_init(&sm.full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_read[i], 256);
-      mbar_init(&sm.ds_ready[i], 256);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.dp_full[i], 1);
+      mbar_init(&sm.s_read[i], kGroupThreads);
+      mbar_init(&sm.ds_ready[i], kGroupThreads);
+      mbar_init(&sm.ds_used[i], 1);
     }
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain, 2);
     mbar_init(&sm.dirty, 1);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
@@ -523,9 +568,13 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
+  const int lo = min(min(sm.lo[0], sm.lo[1]), min(sm.lo[2], sm.lo[3]));
+  const int hi = max(max(sm.hi[0], sm.hi[1]), max(sm.hi[2], sm.hi[3]));
+  const int n = lo < hi ? (hi - lo + kStep - 1) / kStep : 0, base = n > 0 ? lo : 0;
+  const int n_last = hi - (base + (n - 1) * kStep);             // keys of the union in the last step
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
     if (warp == 0 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ producer
       mbar_arrive_expect_tx(&sm.q_full, 2 * kTileBytes);
@@ -534,118 +583,125 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       for (int j = 0; j < n; ++j) {
         const int s = j % kStages;
         if (j >= kStages && !mbar_wait(&sm.kv_empty[s], ((j / kStages) - 1) & 1, abort, st)) break;
-        mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kTileBytes);
-        tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kAttnTile, kh, b);
-        tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kAttnTile, kh, b);
+        mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kStepBytes);
+        tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kStep, kh, b);
+        tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kStep, kh, b);
       }
     } else if (warp == 1 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ MMA issue
-      auto issue_s = [&](int j) -> bool {
-        const int s = j % kStages;
-        if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
-        if (j == n - 1 && n_last < kAttnTile) {
-          mbar_arrive(&sm.dirty);
-          if (!mbar_wait(&sm.clean, 0, abort, st)) return false;
-        }
-        tc_fence_after();
-        mma_rows(tmem + ((2 * j) % 3) * 128, sm.q, sm.k[s]);
-        umma_commit(&sm.full[(2 * j) % 3]);
-        return true;
-      };
-      auto issue_dp = [&](int j) {
-        mma_rows(tmem + ((2 * j + 1) % 3) * 128, sm.g, sm.v[j % kStages]);
-        umma_commit(&sm.full[(2 * j + 1) % 3]);
-      };
+      // ------------------------------------------------------------ S and dP
       bool ok = mbar_wait(&sm.q_full, 0, abort, st);
-      if (ok) ok = issue_s(0);
-      if (ok) issue_dp(0);
-      if (ok && n > 1) ok = issue_s(1);
       for (int j = 0; ok && j < n; ++j) {
-        if (!mbar_wait(&sm.s_read[j & 1], (j >> 1) & 1, abort, st)) break;
+        const int s = j % kStages, g = j & 1, m = j >> 1;
+        if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) break;
+        if (j == n - 1 && n_last < kStep) {
+          mbar_arrive(&sm.dirty);
+          if (!mbar_wait(&sm.clean, 0, abort, st)) break;
+        }
+        if (m > 0 && !mbar_wait(&sm.s_read[g], (m - 1) & 1, abort, st)) break;
         tc_fence_after();
-        if (j + 1 < n) issue_dp(j + 1);                         // into the buffer S_j was read from
-        if (!mbar_wait(&sm.ds_ready[j & 1], (j >> 1) & 1, abort, st)) break;
+        mma_rows(tmem + g * 2 * kStep, sm.q, sm.k[s]);
+        umma_commit(&sm.s_full[g]);
+        if (m > 0 && !mbar_wait(&sm.ds_used[g], (m - 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_cols(tmem + kColA, tmem + ((2 * j + 1) % 3) * 128, sm.k[j % kStages], j > 0);
-        umma_commit(&sm.kv_empty[j % kStages]);
-        if (j + 2 < n) ok = issue_s(j + 2);                     // into the buffer dQ_j reads from
+        mma_rows(tmem + g * 2 * kStep + kStep, sm.g, sm.v[s]);
+        umma_commit(&sm.dp_full[g]);
       }
       umma_commit(&sm.drain);
       drain_mma(&sm.drain, 0);
-    } else if (warp == 2 && n > 0 && n_last < kAttnTile) {
+    } else if (warp == 3 && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ dQ += dS K
+      for (int j = 0; j < n; ++j) {
+        const int s = j % kStages, g = j & 1, m = j >> 1;
+        if (!mbar_wait(&sm.ds_ready[g], m & 1, abort, st)) break;
+        tc_fence_after();
+        mma_cols(tmem + kColA, tmem + g * 2 * kStep + kStep, sm.k[s], j > 0);
+        umma_commit(&sm.ds_used[g]);
+        umma_commit(&sm.kv_empty[s]);
+      }
+      umma_commit(&sm.drain);
+      drain_mma(&sm.drain, 0);
+    } else if (warp == 2 && n > 0 && n_last < kStep) {
       // ------------------------------------------------------------ K rows behind the union of the ranges
       const int s = (n - 1) % kStages;
       if (__all_sync(0xffffffffu, mbar_wait(&sm.dirty, 0, abort, st)) &&
           __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n - 1) / kStages) & 1, abort, st))) {
-        zero_rows(sm.k[s], [&](int r) { return r >= n_last; });
+        zero_rows(sm.k[s], kStep, [&](int r) { return r >= n_last; });
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.clean);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
     // ------------------------------------------------------------ dS
-    const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const int l = qt * kAttnTile + row;                         // below Lp
-    const float m = nlse[(size_t)bh * Lp + l], nd = ndsum[(size_t)bh * Lp + l];
-    const int2 keys = ranges[b * Lp + l];
-    const bool live = keys.x < keys.y;
-    const int f_lo = warp_max(live ? keys.x : 0) - base - wg * 64;   // every live row of the warp sees [f_lo, f_hi)
-    const int f_hi = warp_min(live ? keys.y : 0x7fffffff) - base - wg * 64;
-    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), mm = f2_pack(m, m), dd = f2_pack(nd, nd);
+    const uint32_t ts = tmem + lane_off + grp * 2 * kStep + half * kCols, td = ts + kStep;
+    const float m2 = l < a.L ? nlse[(size_t)bh * Lp + l] : -INFINITY, nd = l < a.L ? ndsum[(size_t)bh * Lp + l] : 0.f;
+    const int c0 = base + half * kCols;                         // the key of this thread's first column in step 0
+    const int f_lo = warp_max(live ? keys.x : 0) - c0;          // every live row of the warp sees [f_lo, f_hi)
+    const int f_hi = warp_min(live ? keys.y : 0x7fffffff) - c0;
+    const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), mm = f2_pack(m2, m2), dd = f2_pack(nd, nd);
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t ts = tmem + lane_off + ((2 * j) % 3) * 128 + wg * 64;
-      const uint32_t td = tmem + lane_off + ((2 * j + 1) % 3) * 128 + wg * 64;
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * j) % 3], ((2 * j) / 3) & 1, abort, st))) { ok = false; break; }
+    for (int j = grp; j < n; j += 2) {
+      const int m = j >> 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], m & 1, abort, st))) { ok = false; break; }
       tc_fence_after();
-      uint32_t p[64];
-      tmem_ld64(ts, p);
+      uint32_t p[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
+      tmem_wait_ld();
       tc_fence_before();
-      mbar_arrive(&sm.s_read[j & 1]);
-      const bool masked = f_lo > j * kAttnTile || f_hi < j * kAttnTile + 64;
+      mbar_arrive(&sm.s_read[grp]);
+      const bool masked = f_lo > j * kStep || f_hi < j * kStep + kCols;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc, mm);
+      for (int e = 0; e < kCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc, mm);
       if (masked) {
-        const int first = keys.x - base - wg * 64 - j * kAttnTile, last = keys.y - base - wg * 64 - j * kAttnTile;
+        const int first = keys.x - c0 - j * kStep, last = keys.y - c0 - j * kStep;
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
+        for (int e = 0; e < kCols; ++e)
           if (e < first || e >= last) p[e] = 0u;
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[(2 * j + 1) % 3], ((2 * j + 1) / 3) & 1, abort, st))) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.dp_full[grp], m & 1, abort, st))) { ok = false; break; }
       tc_fence_after();
-      uint32_t g[64], pk[32];
-      tmem_ld64(td, g);
-      if (masked) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (p[e] == 0u) g[e] = 0u;                            // a value nobody sees may be NaN
+      for (int c = 0; c < kCols; c += kChunk) {
+        uint32_t g[16], pk[8];
+        tmem_ld16(td + c, g);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (p[c + e] == 0u) g[e] = 0u;                      // a value nobody sees may be NaN
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = ds_pair(p[c + 2 * e], p[c + 2 * e + 1], g[2 * e], g[2 * e + 1], dd);
+        tmem_st8(td + c / 2, pk);
       }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) pk[e] = ds_pair(p[2 * e], p[2 * e + 1], g[2 * e], g[2 * e + 1], dd);
-      tmem_st32(td, pk);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sm.ds_ready[j & 1]);
+      mbar_arrive(&sm.ds_ready[grp]);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
     tc_fence_after();
     if (ok) {
-      uint32_t o[32];                                           // each warpgroup stores 32 channels
+      // each of the 2 kHalves warpgroups stores its channels
+      constexpr int kOut = kAttnD / (2 * kHalves);
+      const int o0 = (grp * kHalves + half) * kOut;
+      uint32_t o[kOut];
       if (n > 0) {
-        tmem_ld32(tmem + lane_off + kColA + wg * 32, o);
+#pragma unroll
+        for (int c = 0; c < kOut; c += 16)
+          tmem_ld16(tmem + lane_off + kColA + o0 + c, *reinterpret_cast<uint32_t(*)[16]>(&o[c]));
         tmem_wait_ld();
       }
       if (n == 0 || !live) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0u;
+        for (int e = 0; e < kOut; ++e) o[e] = 0u;
       }
       if (l < a.L) {
         __nv_bfloat16* dst =
             reinterpret_cast<__nv_bfloat16*>(a.dq.data) + b * a.dq.sb + h * a.dq.sh + (int64_t)l * a.dq.st;
-        store_row_bf16<4>(o, dst, a.scale, wg * 32, a.d);
+        store_row_bf16<kOut / 8>(o, dst, a.scale, o0, a.d);
       }
     }
   }
@@ -668,9 +724,9 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // their steps plus about three steps of start and end.
 AttnBwdPlan attn_bwd_plan(const httm_attention& a) {
   AttnBwdPlan p{};
-  p.q_tiles = (a.q_len + kAttnTile - 1) / kAttnTile;
+  p.q_tiles = (a.q_len + kStep - 1) / kStep;
   p.k_tiles = (a.kv_len + kAttnTile - 1) / kAttnTile;
-  p.Lp = p.q_tiles * kAttnTile;
+  p.Lp = p.q_tiles * kStep;
   const long long items = (long long)a.batch * a.kv_heads * p.k_tiles;
   const long long steps = (long long)(a.heads / a.kv_heads) * p.q_tiles;
   p.kv_parts = 1;
@@ -705,9 +761,11 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, c
   AttnMap mq, mg, mk, mv;
   // with no queries (or no keys) nothing is loaded through their maps
   const void* any = a.L > 0 ? a.q.data : a.k.data;
-  if (!attn_map(&mq, a.q, any, a.d, a.L, a.H, a.B) || !attn_map(&mg, a.dout, any, a.d, a.L, a.H, a.B) ||
-      !attn_map(&mk, a.k, any, a.d, a.N, a.K, a.B) || !attn_map(&mv, a.v, any, a.d, a.N, a.K, a.B))
-    return cudaErrorInvalidValue;
+  auto maps = [&](int q_box, int kv_box) {
+    return attn_map(&mq, a.q, any, a.d, a.L, a.H, a.B, q_box) && attn_map(&mg, a.dout, any, a.d, a.L, a.H, a.B, q_box) &&
+           attn_map(&mk, a.k, any, a.d, a.N, a.K, a.B, kv_box) && attn_map(&mv, a.v, any, a.d, a.N, a.K, a.B, kv_box);
+  };
+  if (!maps(kStep, kAttnTile)) return cudaErrorInvalidValue;
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDkvSmem)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem)) != cudaSuccess)
@@ -727,9 +785,11 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, c
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
   }
-  if (p.q_tiles > 0)
-    attn_dq_kernel<<<(unsigned)((long long)a.B * a.H * p.q_tiles), kThreads, kDqSmem, s>>>(mq, mg, mk, mv, a, p.q_tiles,
-                                                                                         nlse, ndsum, ranges, tiles);
+  if (!maps(kAttnTile, kStep)) return cudaErrorInvalidValue;
+  const long long m_tiles = (a.L + kAttnTile - 1) / kAttnTile;
+  if (m_tiles > 0)
+    attn_dq_kernel<<<(unsigned)(a.B * a.H * m_tiles), kThreads, kDqSmem, s>>>(mq, mg, mk, mv, a, p.q_tiles,
+                                                                                         nlse, ndsum, ranges);
   return cudaGetLastError();
 }
 

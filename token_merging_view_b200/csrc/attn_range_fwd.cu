@@ -179,7 +179,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       const int s = (n_kv - 1) % kStages;
       if (__all_sync(0xffffffffu, mbar_wait(&sm.dirty, 0, abort, st)) &&
           __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n_kv - 1) / kStages) & 1, abort, st))) {
-        zero_rows(sm.v[s], [&](int r) { return r >= n_last; });
+        zero_rows(sm.v[s], kAttnTile, [&](int r) { return r >= n_last; });
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.clean);
@@ -436,7 +436,8 @@ AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
 cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s) {
   AttnMap mk, mv;
   // without keys nothing is loaded through their maps
-  if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B) || !attn_map(&mv, a.v, a.q.data, a.d, a.N, a.K, a.B))
+  if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B, kAttnTile) ||
+      !attn_map(&mv, a.v, a.q.data, a.d, a.N, a.K, a.B, kAttnTile))
     return cudaErrorInvalidValue;
   cudaError_t e =
       cudaFuncSetAttribute(attn_range_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
