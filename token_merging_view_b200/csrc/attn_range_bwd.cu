@@ -24,11 +24,14 @@
 // (2 x 2 x 96 columns; the accumulators take the other 128), so that one
 // group exponentiates while the other forms dS, and neither waits for a
 // buffer of the other.  P overwrites its S and dS its dP, as bf16 pairs.
-// Warp 0 loads (TMA), warp 1 issues the products S and dP, warp 3 those that
-// P and dS enter: one thread issues an N = 64 product at half the tensor
-// core's rate, two keep it fed; each accumulator has one issuing thread, so
-// its order of summation is fixed.  Warp 2 clears loaded rows that may hold
-// anything.  A group is kHalves warpgroups of 4 warps (TMEM lane = row),
+// Warp 0 loads (TMA); one thread of warp 1 and one of warp 3 issue the MMAs:
+// one alone issues an N = 64 product at half the tensor core's rate, two
+// keep it fed.  They share the work so that a product which overwrites an
+// operand is issued by the thread that issued that operand's use (the tensor
+// core works in order of issue per thread), and so that every accumulator
+// has one issuing thread: its order of summation is fixed.  For dK and dV
+// warp 1 has S and dV, warp 3 dP and dK; for dQ each has a group, with an
+// accumulator of its own.  Warp 2 clears loaded rows that may hold anything.  A group is kHalves warpgroups of 4 warps (TMEM lane = row),
 // each with 96 / kHalves of the columns.
 //
 // Parity waits: a barrier of a group completes one phase per step of that
@@ -51,10 +54,15 @@ constexpr int kCols = kStep / kHalves;                // columns of a thread
 constexpr int kChunk = 16;                            // columns in registers at a time
 constexpr int kGroupThreads = kHalves * 128;
 constexpr int kThreads = 128 + 2 * kGroupThreads;
+// registers a thread: launched at 65,536 / kThreads (a multiple of 8), then
+// 128 kAuxRegs + 2 kGroupThreads kWorkRegs of the same total
+constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+constexpr int kWorkRegs = kHalves == 2 ? 104 : 208, kAuxRegs = kHalves == 2 ? 64 : 88;
+static_assert(128 * kAuxRegs + 2 * kGroupThreads * kWorkRegs <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kStepBytes = kStep * kAttnD * 2;   // 12 KB
 constexpr int kMaxQTiles = (kAttnMaxQ + kStep - 1) / kStep;
 constexpr int kMaxWords = (kMaxQTiles + 31) / 32;
-constexpr uint32_t kColA = 384, kColB = 448;          // accumulators (dV, dK; dQ in kColA)
+constexpr uint32_t kColA = 384, kColB = 448;          // accumulators: dV and dK, or the two groups' dQ
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kCols % kChunk == 0 && kCols % 16 == 0, "whole chunks, whole K steps");
 
@@ -121,25 +129,25 @@ attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restr
   }
 }
 
+// Descriptor of a tile; K steps only add to its address field (shared memory
+// addresses in 16-byte units stay below the field's 14 bits).
+__device__ __forceinline__ uint64_t tile_desc(const uint8_t* tile) { return sw128_desc(smem_u32(tile), 1024); }
+
 // D = A B^T: K-major tiles of 128 and of 96 rows x 64 channels.
-__device__ __forceinline__ void mma_rows(uint32_t d, const uint8_t* A, const uint8_t* B) {
+__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t A, uint64_t B) {
   constexpr uint32_t id = idesc_bf16(128, kStep, false, false);
-  const uint32_t x = smem_u32(A), y = smem_u32(B);
 #pragma unroll
-  for (int kk = 0; kk < kAttnD / 16; ++kk)
-    umma_bf16(d, sw128_desc(x + kk * 32, 1024), sw128_desc(y + kk * 32, 1024), id, kk > 0);
+  for (int kk = 0; kk < kAttnD / 16; ++kk) umma_bf16(d, A + kk * 2, B + kk * 2, id, kk > 0);
 }
 // D (+)= A B: A the 128 x 96 P or dS that the warpgroups of a group wrote to
 // the front of their columns of the product at `A`; B a tile of 96 rows x 64
 // channels.
-__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, const uint8_t* B, bool add) {
+__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, uint64_t B, bool add) {
   constexpr uint32_t id = idesc_bf16(128, kAttnD, false, true);
   constexpr int per = kCols / 16;                     // K steps of one warpgroup's columns
-  const uint32_t y = smem_u32(B);
 #pragma unroll
   for (int kk = 0; kk < kStep / 16; ++kk)
-    umma_bf16_ts(d, A + (kk / per) * kCols + (kk % per) * 8, sw128_desc(y + kk * 16 * 128, 1024), id,
-                 (add || kk > 0) ? 1u : 0u);
+    umma_bf16_ts(d, A + (kk / per) * kCols + (kk % per) * 8, B + kk * 128, id, (add || kk > 0) ? 1u : 0u);
 }
 
 // Two neighbouring scores: s -> 2^(s c + m).
@@ -165,7 +173,7 @@ struct DkvSmem {
   int2 range[kStages][kStep];
   uint32_t active[kMaxWords], masked[kMaxWords], dead[kMaxWords];
   uint64_t kv_full, q_full[kStages], q_empty[kStages];
-  uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2], p_used[2], ds_used[2], drain, dirty, clean;
+  uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2], drain, dirty, clean;
   int count[kThreads / 32];
   uint32_t tmem_base;
   int abort;
@@ -249,18 +257,16 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
     mbar_init(&sm.kv_full, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.q_full[s], 1);
-      mbar_init(&sm.q_empty[s], 1);
+      mbar_init(&sm.q_empty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.dp_full[i], 1);
       mbar_init(&sm.p_ready[i], kGroupThreads);
       mbar_init(&sm.ds_ready[i], kGroupThreads);
-      mbar_init(&sm.p_used[i], 1);
-      mbar_init(&sm.ds_used[i], 1);
     }
     mbar_init(&sm.drain, 2);
-    mbar_init(&sm.dirty, 1);
+    mbar_init(&sm.dirty, 2);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
     mbar_fence_init();
@@ -278,7 +284,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
   const int s0 = (int)(all * part / parts), n = (int)(all * (part + 1) / parts) - s0;   // steps of this CTA
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs) : "memory");
     if (warp == 0 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ producer
       mbar_arrive_expect_tx(&sm.kv_full, 2 * kTileBytes);
@@ -296,44 +302,40 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         bulk_load(sm.ndsum[s], ndsum + at, kStep * 4, &sm.q_full[s]);
         bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kStep, kStep * 8, &sm.q_full[s]);
       }
-    } else if (warp == 1 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ S^T and dP^T
+    } else if ((warp == 1 || warp == 3) && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ MMA issue
+      // warp 1: S^T = K Q^T and dV += P^T dO; warp 3: dP^T = V dO^T and dK +=
+      // dS^T Q.  A group's next S (dP) overwrites the P (dS) it follows.
+      const bool first = warp == 1;
+      const uint64_t own = tile_desc(first ? sm.k : sm.v);
+      const uint64_t rows = tile_desc(first ? sm.q[0] : sm.g[0]), cols = tile_desc(first ? sm.g[0] : sm.q[0]);
+      const uint32_t buf = tmem + (first ? 0 : kStep), acc = tmem + (first ? kColA : kColB);
+      uint64_t* full = first ? sm.s_full : sm.dp_full;
+      uint64_t* ready = first ? sm.p_ready : sm.ds_ready;
       TileWalk walk(sm.active, words, n_active, s0);
       int n_dirty = 0;
-      bool ok = mbar_wait(&sm.kv_full, 0, abort, st);
-      for (int i = 0; ok && i < n; ++i) {
-        const int s = i % kStages, t = walk.next(), grp = i & 1, m = i >> 1;
-        if (!mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) break;
+      auto product = [&](int i) -> bool {
+        const int s = i % kStages, t = walk.next(), grp = i & 1;
+        if (!mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) return false;
         if (sm.dead[t >> 5] >> (t & 31) & 1) {                  // rows that may hold anything
           mbar_arrive(&sm.dirty);
-          if (!mbar_wait(&sm.clean, n_dirty++ & 1, abort, st)) break;
+          if (!mbar_wait(&sm.clean, n_dirty++ & 1, abort, st)) return false;
         }
-        if (m > 0 && !mbar_wait(&sm.p_used[grp], (m - 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_rows(tmem + grp * 2 * kStep, sm.k, sm.q[s]);
-        umma_commit(&sm.s_full[grp]);
-        if (m > 0 && !mbar_wait(&sm.ds_used[grp], (m - 1) & 1, abort, st)) break;
+        mma_rows(buf + grp * 2 * kStep, own, rows + s * (kStepBytes >> 4));
+        umma_commit(&full[grp]);
+        return true;
+      };
+      bool ok = mbar_wait(&sm.kv_full, 0, abort, st) && product(0) && (n == 1 || product(1));
+      for (int i = 0; ok && i < n; ++i) {
+        const int s = i % kStages, grp = i & 1;
+        if (!mbar_wait(&ready[grp], (i >> 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_rows(tmem + grp * 2 * kStep + kStep, sm.v, sm.g[s]);
-        umma_commit(&sm.dp_full[grp]);
-      }
-      umma_commit(&sm.drain);
-      drain_mma(&sm.drain, 0);
-    } else if (warp == 3 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ dV += P^T dO, dK += dS^T Q
-      for (int i = 0; i < n; ++i) {
-        const int s = i % kStages, grp = i & 1, m = i >> 1;
-        if (!mbar_wait(&sm.p_ready[grp], m & 1, abort, st)) break;
-        tc_fence_after();
-        mma_cols(tmem + kColA, tmem + grp * 2 * kStep, sm.g[s], i > 0);
-        umma_commit(&sm.p_used[grp]);
-        if (!mbar_wait(&sm.ds_ready[grp], m & 1, abort, st)) break;
-        tc_fence_after();
-        mma_cols(tmem + kColB, tmem + grp * 2 * kStep + kStep, sm.q[s], i > 0);
-        umma_commit(&sm.ds_used[grp]);
+        mma_cols(acc, buf + grp * 2 * kStep, cols + s * (kStepBytes >> 4), i > 0);
         umma_commit(&sm.q_empty[s]);
+        if (i + 2 < n) ok = product(i + 2);
       }
-      umma_commit(&sm.drain);
+      umma_commit(&sm.drain);                                   // every MMA ends before TMEM is released
       drain_mma(&sm.drain, 0);
     } else if (warp == 2 && n > 0) {
       // ------------------------------------------------------------ rows that see nothing
@@ -342,7 +344,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       for (int i = 0; i < n; ++i) {
         const int s = i % kStages, t = walk.next();
         if (!(sm.dead[t >> 5] >> (t & 31) & 1)) continue;
-        // the issuing thread says when the stage is there, and waits
+        // both issuing threads say when they have reached the step, and wait
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.dirty, n_dirty++ & 1, abort, st)) ||
             !__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)))
           break;
@@ -354,7 +356,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegs) : "memory");
     // ------------------------------------------------------------ P and dS
     const int grp = (warp - 4) / (4 * kHalves), half = ((warp - 4) >> 2) % kHalves, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -509,7 +511,7 @@ struct DqSmem {
   uint8_t q[kTileBytes], g[kTileBytes];
   uint8_t k[kStages][kStepBytes], v[kStages][kStepBytes];
   uint64_t q_full, kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], dp_full[2], s_read[2], ds_ready[2], ds_used[2], drain, dirty, clean;
+  uint64_t s_full[2], dp_full[2], s_read[2], ds_ready[2], drain, dirty, clean;
   int lo[4], hi[4];
   uint32_t tmem_base;
   int abort;
@@ -554,7 +556,6 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       mbar_init(&sm.dp_full[i], 1);
       mbar_init(&sm.s_read[i], kGroupThreads);
       mbar_init(&sm.ds_ready[i], kGroupThreads);
-      mbar_init(&sm.ds_used[i], 1);
     }
     mbar_init(&sm.drain, 2);
     mbar_init(&sm.dirty, 1);
@@ -574,7 +575,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
   const int n_last = hi - (base + (n - 1) * kStep);             // keys of the union in the last step
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs) : "memory");
     if (warp == 0 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ producer
       mbar_arrive_expect_tx(&sm.q_full, 2 * kTileBytes);
@@ -587,38 +588,42 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
         tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kStep, kh, b);
         tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kStep, kh, b);
       }
-    } else if (warp == 1 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ S and dP
-      bool ok = mbar_wait(&sm.q_full, 0, abort, st);
-      for (int j = 0; ok && j < n; ++j) {
-        const int s = j % kStages, g = j & 1, m = j >> 1;
-        if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) break;
+    } else if ((warp == 1 || warp == 3) && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ MMA issue
+      // warp 1 for the first group, warp 3 for the second: S = Q K^T, dP = dO
+      // V^T, dQ_g += dS K, each group with its own accumulator
+      const int g = warp >> 1;
+      const uint64_t qd = tile_desc(sm.q), gd = tile_desc(sm.g), kd = tile_desc(sm.k[0]), vd = tile_desc(sm.v[0]);
+      const uint32_t buf = tmem + g * 2 * kStep, acc = tmem + (g ? kColB : kColA);
+      auto issue_s = [&](int j) -> bool {
+        const int s = j % kStages;
+        if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
         if (j == n - 1 && n_last < kStep) {
           mbar_arrive(&sm.dirty);
-          if (!mbar_wait(&sm.clean, 0, abort, st)) break;
+          if (!mbar_wait(&sm.clean, 0, abort, st)) return false;
         }
-        if (m > 0 && !mbar_wait(&sm.s_read[g], (m - 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_rows(tmem + g * 2 * kStep, sm.q, sm.k[s]);
+        mma_rows(buf, qd, kd + s * (kStepBytes >> 4));
         umma_commit(&sm.s_full[g]);
-        if (m > 0 && !mbar_wait(&sm.ds_used[g], (m - 1) & 1, abort, st)) break;
-        tc_fence_after();
-        mma_rows(tmem + g * 2 * kStep + kStep, sm.g, sm.v[s]);
+        return true;
+      };
+      auto issue_dp = [&](int j) {
+        mma_rows(buf + kStep, gd, vd + (j % kStages) * (kStepBytes >> 4));
         umma_commit(&sm.dp_full[g]);
-      }
-      umma_commit(&sm.drain);
-      drain_mma(&sm.drain, 0);
-    } else if (warp == 3 && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ dQ += dS K
-      for (int j = 0; j < n; ++j) {
-        const int s = j % kStages, g = j & 1, m = j >> 1;
+      };
+      bool ok = g < n && mbar_wait(&sm.q_full, 0, abort, st) && issue_s(g);
+      if (ok) issue_dp(g);
+      for (int j = g; ok && j < n; j += 2) {
+        const int m = j >> 1;
+        if (!mbar_wait(&sm.s_read[g], m & 1, abort, st)) break;
+        if (j + 2 < n && !issue_s(j + 2)) break;
         if (!mbar_wait(&sm.ds_ready[g], m & 1, abort, st)) break;
         tc_fence_after();
-        mma_cols(tmem + kColA, tmem + g * 2 * kStep + kStep, sm.k[s], j > 0);
-        umma_commit(&sm.ds_used[g]);
-        umma_commit(&sm.kv_empty[s]);
+        mma_cols(acc, buf + kStep, kd + (j % kStages) * (kStepBytes >> 4), m > 0);
+        umma_commit(&sm.kv_empty[j % kStages]);
+        if (j + 2 < n) issue_dp(j + 2);                         // over the dS that dQ reads
       }
-      umma_commit(&sm.drain);
+      umma_commit(&sm.drain);                                   // every MMA ends before TMEM is released
       drain_mma(&sm.drain, 0);
     } else if (warp == 2 && n > 0 && n_last < kStep) {
       // ------------------------------------------------------------ K rows behind the union of the ranges
@@ -632,7 +637,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegs) : "memory");
     // ------------------------------------------------------------ dS
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_off + grp * 2 * kStep + half * kCols, td = ts + kStep;
@@ -693,6 +698,15 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
         for (int c = 0; c < kOut; c += 16)
           tmem_ld16(tmem + lane_off + kColA + o0 + c, *reinterpret_cast<uint32_t(*)[16]>(&o[c]));
         tmem_wait_ld();
+      }
+      if (n > 1) {                                              // the second group's sum
+        uint32_t x[kOut];
+#pragma unroll
+        for (int c = 0; c < kOut; c += 16)
+          tmem_ld16(tmem + lane_off + kColB + o0 + c, *reinterpret_cast<uint32_t(*)[16]>(&x[c]));
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x[e]));
       }
       if (n == 0 || !live) {
 #pragma unroll
