@@ -19,6 +19,25 @@ __device__ __forceinline__ void tma_load_tile(void* dst, const AttnMap& m, uint6
       : "memory");
 }
 
+// One lane of a converged warp, always the same one; the compiler knows the
+// branch for what it is and keeps the operands of the MMAs in it uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// A value that every lane holds, as one the compiler can treat so.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// A wait of a whole warp, with a result the compiler knows to be uniform.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, DevState* st) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, st));
+}
+
 // A plain bulk copy; addresses and size are multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(

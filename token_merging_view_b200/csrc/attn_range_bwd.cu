@@ -47,7 +47,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kStages = 4;
+constexpr int kStages = 4;                            // query tiles in flight (dK, dV)
+constexpr int kKvStages = 6;                          // key tiles in flight (dQ)
 constexpr int kStep = kAttnStep;
 constexpr int kHalves = 2;                            // warpgroups of a group
 constexpr int kCols = kStep / kHalves;                // columns of a thread
@@ -223,7 +224,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
                 const AttnTileRange* __restrict__ tiles, float* __restrict__ part_out) {
   extern __shared__ uint8_t smem_raw[];
   DkvSmem& sm = *reinterpret_cast<DkvSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const unsigned item = blockIdx.x / parts, part = blockIdx.x % parts;
   const int bk = item / k_tiles, kt = item % k_tiles, b = bk / a.K, kh = bk % a.K;
   const int k0 = kt * kAttnTile, k1 = min(k0 + kAttnTile, a.N);
@@ -281,7 +282,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) n_active += sm.count[w];
   const long long all = (long long)n_active * a.G;
-  const int s0 = (int)(all * part / parts), n = (int)(all * (part + 1) / parts) - s0;   // steps of this CTA
+  const int s0 = (int)(all * part / parts), n = uniform((int)(all * (part + 1) / parts) - s0);   // steps of this CTA
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs) : "memory");
@@ -302,7 +303,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         bulk_load(sm.ndsum[s], ndsum + at, kStep * 4, &sm.q_full[s]);
         bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kStep, kStep * 8, &sm.q_full[s]);
       }
-    } else if ((warp == 1 || warp == 3) && lane == 0 && n > 0) {
+    } else if ((warp == 1 || warp == 3) && n > 0) {
       // ------------------------------------------------------------ MMA issue
       // warp 1: S^T = K Q^T and dV += P^T dO; warp 3: dP^T = V dO^T and dK +=
       // dS^T Q.  A group's next S (dP) overwrites the P (dS) it follows.
@@ -316,27 +317,40 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       int n_dirty = 0;
       auto product = [&](int i) -> bool {
         const int s = i % kStages, t = walk.next(), grp = i & 1;
-        if (!mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) return false;
-        if (sm.dead[t >> 5] >> (t & 31) & 1) {                  // rows that may hold anything
-          mbar_arrive(&sm.dirty);
-          if (!mbar_wait(&sm.clean, n_dirty++ & 1, abort, st)) return false;
+        if (!wait_all(&sm.q_full[s], (i / kStages) & 1, abort, st)) return false;
+        if (__any_sync(0xffffffffu, sm.dead[t >> 5] >> (t & 31) & 1)) {   // rows that may hold anything
+          if (lane == 0) mbar_arrive(&sm.dirty);
+          if (!wait_all(&sm.clean, n_dirty++ & 1, abort, st)) return false;
         }
         tc_fence_after();
-        mma_rows(buf + grp * 2 * kStep, own, rows + s * (kStepBytes >> 4));
-        umma_commit(&full[grp]);
+        const uint64_t desc = rows + s * (kStepBytes >> 4);
+        const uint32_t d = buf + grp * 2 * kStep;
+        if (elect_one()) {
+          mma_rows(d, own, desc);
+          umma_commit(&full[grp]);
+        }
+        __syncwarp();
         return true;
       };
-      bool ok = mbar_wait(&sm.kv_full, 0, abort, st) && product(0) && (n == 1 || product(1));
+      bool ok = wait_all(&sm.kv_full, 0, abort, st) && product(0) && (n == 1 || product(1));
       for (int i = 0; ok && i < n; ++i) {
         const int s = i % kStages, grp = i & 1;
-        if (!mbar_wait(&ready[grp], (i >> 1) & 1, abort, st)) break;
+        if (!wait_all(&ready[grp], (i >> 1) & 1, abort, st)) break;
         tc_fence_after();
-        mma_cols(acc, buf + grp * 2 * kStep, cols + s * (kStepBytes >> 4), i > 0);
-        umma_commit(&sm.q_empty[s]);
+        const uint64_t desc = cols + s * (kStepBytes >> 4);
+        const uint32_t A = buf + grp * 2 * kStep;
+        if (elect_one()) {
+          mma_cols(acc, A, desc, i > 0);
+          umma_commit(&sm.q_empty[s]);
+        }
+        __syncwarp();
         if (i + 2 < n) ok = product(i + 2);
       }
-      umma_commit(&sm.drain);                                   // every MMA ends before TMEM is released
-      drain_mma(&sm.drain, 0);
+      if (elect_one()) {
+        umma_commit(&sm.drain);                                 // every MMA ends before TMEM is released
+        drain_mma(&sm.drain, 0);
+      }
+      __syncwarp();
     } else if (warp == 2 && n > 0) {
       // ------------------------------------------------------------ rows that see nothing
       TileWalk walk(sm.active, words, n_active, s0);
@@ -509,8 +523,8 @@ attn_dkv_join_kernel(const __grid_constant__ AttnArgs a, int k_tiles, int parts,
 // ------------------------------------------------------------------ dQ
 struct DqSmem {
   uint8_t q[kTileBytes], g[kTileBytes];
-  uint8_t k[kStages][kStepBytes], v[kStages][kStepBytes];
-  uint64_t q_full, kv_full[kStages], kv_empty[kStages];
+  uint8_t k[kKvStages][kStepBytes], v[kKvStages][kStepBytes];
+  uint64_t q_full, kv_full[kKvStages], kv_empty[kKvStages];
   uint64_t s_full[2], dp_full[2], s_read[2], ds_ready[2], drain, dirty, clean;
   int lo[4], hi[4];
   uint32_t tmem_base;
@@ -526,7 +540,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
                const float* __restrict__ ndsum, const int2* __restrict__ ranges) {
   extern __shared__ uint8_t smem_raw[];
   DqSmem& sm = *reinterpret_cast<DqSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int m_tiles = (a.L + kAttnTile - 1) / kAttnTile;        // tiles of 128 queries; later ones first
   const int bh = blockIdx.x / m_tiles, qt = m_tiles - 1 - blockIdx.x % m_tiles;
   const int b = bh / a.H, h = bh % a.H, kh = h / a.G;
@@ -547,7 +561,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, 1);
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kKvStages; ++s) {
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
@@ -571,7 +585,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
   volatile int* abort = &sm.abort;
   const int lo = min(min(sm.lo[0], sm.lo[1]), min(sm.lo[2], sm.lo[3]));
   const int hi = max(max(sm.hi[0], sm.hi[1]), max(sm.hi[2], sm.hi[3]));
-  const int n = lo < hi ? (hi - lo + kStep - 1) / kStep : 0, base = n > 0 ? lo : 0;
+  const int n = uniform(lo < hi ? (hi - lo + kStep - 1) / kStep : 0), base = n > 0 ? lo : 0;
   const int n_last = hi - (base + (n - 1) * kStep);             // keys of the union in the last step
 
   if (warp < 4) {
@@ -582,13 +596,13 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       tma_load_tile(sm.q, mq, &sm.q_full, qt * kAttnTile, h, b);
       tma_load_tile(sm.g, mg, &sm.q_full, qt * kAttnTile, h, b);
       for (int j = 0; j < n; ++j) {
-        const int s = j % kStages;
-        if (j >= kStages && !mbar_wait(&sm.kv_empty[s], ((j / kStages) - 1) & 1, abort, st)) break;
+        const int s = j % kKvStages;
+        if (j >= kKvStages && !mbar_wait(&sm.kv_empty[s], ((j / kKvStages) - 1) & 1, abort, st)) break;
         mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kStepBytes);
         tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kStep, kh, b);
         tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kStep, kh, b);
       }
-    } else if ((warp == 1 || warp == 3) && lane == 0 && n > 0) {
+    } else if ((warp == 1 || warp == 3) && n > 0) {
       // ------------------------------------------------------------ MMA issue
       // warp 1 for the first group, warp 3 for the second: S = Q K^T, dP = dO
       // V^T, dQ_g += dS K, each group with its own accumulator
@@ -596,40 +610,55 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       const uint64_t qd = tile_desc(sm.q), gd = tile_desc(sm.g), kd = tile_desc(sm.k[0]), vd = tile_desc(sm.v[0]);
       const uint32_t buf = tmem + g * 2 * kStep, acc = tmem + (g ? kColB : kColA);
       auto issue_s = [&](int j) -> bool {
-        const int s = j % kStages;
-        if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
+        const int s = j % kKvStages;
+        if (!wait_all(&sm.kv_full[s], (j / kKvStages) & 1, abort, st)) return false;
         if (j == n - 1 && n_last < kStep) {
-          mbar_arrive(&sm.dirty);
-          if (!mbar_wait(&sm.clean, 0, abort, st)) return false;
+          if (lane == 0) mbar_arrive(&sm.dirty);
+          if (!wait_all(&sm.clean, 0, abort, st)) return false;
         }
         tc_fence_after();
-        mma_rows(buf, qd, kd + s * (kStepBytes >> 4));
-        umma_commit(&sm.s_full[g]);
+        const uint64_t desc = kd + s * (kStepBytes >> 4);
+        if (elect_one()) {
+          mma_rows(buf, qd, desc);
+          umma_commit(&sm.s_full[g]);
+        }
+        __syncwarp();
         return true;
       };
       auto issue_dp = [&](int j) {
-        mma_rows(buf + kStep, gd, vd + (j % kStages) * (kStepBytes >> 4));
-        umma_commit(&sm.dp_full[g]);
+        const uint64_t desc = vd + (j % kKvStages) * (kStepBytes >> 4);
+        if (elect_one()) {
+          mma_rows(buf + kStep, gd, desc);
+          umma_commit(&sm.dp_full[g]);
+        }
+        __syncwarp();
       };
-      bool ok = g < n && mbar_wait(&sm.q_full, 0, abort, st) && issue_s(g);
+      bool ok = g < n && wait_all(&sm.q_full, 0, abort, st) && issue_s(g);
       if (ok) issue_dp(g);
       for (int j = g; ok && j < n; j += 2) {
-        const int m = j >> 1;
-        if (!mbar_wait(&sm.s_read[g], m & 1, abort, st)) break;
+        const int m = j >> 1, s = j % kKvStages;
+        if (!wait_all(&sm.s_read[g], m & 1, abort, st)) break;
         if (j + 2 < n && !issue_s(j + 2)) break;
-        if (!mbar_wait(&sm.ds_ready[g], m & 1, abort, st)) break;
+        if (!wait_all(&sm.ds_ready[g], m & 1, abort, st)) break;
         tc_fence_after();
-        mma_cols(acc, buf + kStep, kd + (j % kStages) * (kStepBytes >> 4), m > 0);
-        umma_commit(&sm.kv_empty[j % kStages]);
+        const uint64_t desc = kd + s * (kStepBytes >> 4);
+        if (elect_one()) {
+          mma_cols(acc, buf + kStep, desc, m > 0);
+          umma_commit(&sm.kv_empty[s]);
+        }
+        __syncwarp();
         if (j + 2 < n) issue_dp(j + 2);                         // over the dS that dQ reads
       }
-      umma_commit(&sm.drain);                                   // every MMA ends before TMEM is released
-      drain_mma(&sm.drain, 0);
+      if (elect_one()) {
+        umma_commit(&sm.drain);                                 // every MMA ends before TMEM is released
+        drain_mma(&sm.drain, 0);
+      }
+      __syncwarp();
     } else if (warp == 2 && n > 0 && n_last < kStep) {
       // ------------------------------------------------------------ K rows behind the union of the ranges
-      const int s = (n - 1) % kStages;
+      const int s = (n - 1) % kKvStages;
       if (__all_sync(0xffffffffu, mbar_wait(&sm.dirty, 0, abort, st)) &&
-          __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n - 1) / kStages) & 1, abort, st))) {
+          __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n - 1) / kKvStages) & 1, abort, st))) {
         zero_rows(sm.k[s], kStep, [&](int r) { return r >= n_last; });
         fence_async_smem();
         __syncwarp();

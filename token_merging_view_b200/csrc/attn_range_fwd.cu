@@ -63,7 +63,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
                       const __grid_constant__ AttnArgs a, int row_tiles, int parts, float* __restrict__ part_out) {
   extern __shared__ uint8_t smem_raw[];
   FwdSmem& sm = *reinterpret_cast<FwdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   // later rows usually see more keys (causal): they go first
   const unsigned item = blockIdx.x / parts, part = blockIdx.x % parts;
   const int bk = item / row_tiles, rt = row_tiles - 1 - item % row_tiles;
@@ -120,7 +120,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
   // this part's tiles: keys [base, base + 128 n_kv) of [lo, hi)
   const int n_all = hi > lo ? (hi - lo + kAttnTile - 1) / kAttnTile : 0;
   const int j0 = (int)((long long)n_all * part / parts);
-  const int n_kv = (int)((long long)n_all * (part + 1) / parts) - j0;
+  const int n_kv = uniform((int)((long long)n_all * (part + 1) / parts) - j0);
   const int base = n_all > 0 ? lo + j0 * kAttnTile : 0;
   const int n_last = hi - (base + (n_kv - 1) * kAttnTile);   // keys of the union in the last tile
 
@@ -135,45 +135,58 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
         tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kAttnTile, kh, b);
         tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kAttnTile, kh, b);
       }
-    } else if (warp == 1 && lane == 0 && n_kv > 0) {
+    } else if (warp == 1 && n_kv > 0) {
       // ------------------------------------------------------------ MMA issue
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_o = idesc_bf16(128, kAttnD, false, true);
       const int n_prod = n_t * n_kv;                 // S products: i = n_t j + tile
+      const uint64_t qd = sw128_desc(smem_u32(sm.q[0]), 1024), kd = sw128_desc(smem_u32(sm.k[0]), 1024),
+                     vd = sw128_desc(smem_u32(sm.v[0]), 1024);
+      constexpr uint64_t kNext = kTileBytes >> 4;    // from one tile's descriptor to the next one's
       // product i: waits for its K/V tile if it is the tile's first
       auto issue_qk = [&](int i) -> bool {
         const int j = n_t == 2 ? i >> 1 : i, tile = n_t == 2 ? i & 1 : 0, s = j % kStages;
         if (tile == 0) {
-          if (!mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
+          if (!wait_all(&sm.kv_full[s], (j / kStages) & 1, abort, st)) return false;
           if (j == n_kv - 1 && n_last < kAttnTile) {
-            mbar_arrive(&sm.dirty);
-            if (!mbar_wait(&sm.clean, 0, abort, st)) return false;
+            if (lane == 0) mbar_arrive(&sm.dirty);
+            if (!wait_all(&sm.clean, 0, abort, st)) return false;
           }
           tc_fence_after();
         }
-        const uint32_t qa = smem_u32(sm.q[tile]), ka = smem_u32(sm.k[s]), col = tmem + (i % 3) * 128;
+        const uint64_t A = qd + tile * kNext, B = kd + s * kNext;
+        const uint32_t col = tmem + (i % 3) * 128;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAttnD / 16; ++kk)
-          umma_bf16(col, sw128_desc(qa + kk * 32, 1024), sw128_desc(ka + kk * 32, 1024), id_s, kk > 0);
-        umma_commit(&sm.s_full[i % 3]);
+          for (int kk = 0; kk < kAttnD / 16; ++kk) umma_bf16(col, A + kk * 2, B + kk * 2, id_s, kk > 0);
+          umma_commit(&sm.s_full[i % 3]);
+        }
+        __syncwarp();
         return true;
       };
-      bool ok = mbar_wait(&sm.q_full, 0, abort, st);
+      bool ok = wait_all(&sm.q_full, 0, abort, st);
       for (int i = 0; ok && i < min(3, n_prod); ++i) ok = issue_qk(i);
       for (int i = 0; ok && i < n_prod; ++i) {
         const int j = n_t == 2 ? i >> 1 : i, tile = n_t == 2 ? i & 1 : 0, s = j % kStages;
-        if (!mbar_wait(&sm.p_full[tile], j & 1, abort, st)) break;
+        if (!wait_all(&sm.p_full[tile], j & 1, abort, st)) break;
         tc_fence_after();
-        const uint32_t va = smem_u32(sm.v[s]), pc = tmem + (i % 3) * 128, oc = tmem + kColO + tile * 64;
+        const uint64_t B = vd + s * kNext;
+        const uint32_t pc = tmem + (i % 3) * 128, oc = tmem + kColO + tile * 64;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAttnTile / 16; ++kk)
-          umma_bf16_ts(oc, pc + kk * 8, sw128_desc(va + kk * 16 * 128, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&sm.o_done[tile]);
-        if (tile == n_t - 1) umma_commit(&sm.kv_empty[s]);
+          for (int kk = 0; kk < kAttnTile / 16; ++kk)
+            umma_bf16_ts(oc, pc + kk * 8, B + kk * 128, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&sm.o_done[tile]);
+          if (tile == n_t - 1) umma_commit(&sm.kv_empty[s]);
+        }
+        __syncwarp();
         if (i + 3 < n_prod) ok = issue_qk(i + 3);
       }
-      umma_commit(&sm.drain);                        // every MMA ends before TMEM is released
-      drain_mma(&sm.drain, 0);
+      if (elect_one()) {
+        umma_commit(&sm.drain);                      // every MMA ends before TMEM is released
+        drain_mma(&sm.drain, 0);
+      }
+      __syncwarp();
     } else if (warp == 2 && n_kv > 0 && n_last < kAttnTile) {
       // ------------------------------------------------------------ V rows behind the union of the ranges
       const int s = (n_kv - 1) % kStages;
