@@ -43,9 +43,10 @@ struct AttnFwdPlan {
 AttnFwdPlan attn_fwd_plan(const httm_attention& a);
 cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s);
 
-// Backward workspace: per query row lse * log2(e) and D = dout . out, padded
-// to whole tiles, the key range of every query row and of every query tile,
-// then the partial sums of split key tiles.
+// Backward workspace: per query row -lse * log2(e) and -D (D = dout . out),
+// padded to whole steps, both again as tensor-core operands, the key range of
+// every query row and of every step, then the partial sums of split key
+// tiles.
 struct AttnTileRange {
   int lo, hi;      // union of the live rows' ranges (lo >= hi: none)
   int flo, fhi;    // intersection: keys [flo, fhi) are seen by every live row
@@ -55,7 +56,7 @@ struct AttnTileRange {
 struct AttnBwdPlan {
   int q_tiles, k_tiles, Lp;             // tiles of kAttnStep queries, of 128 keys; Lp: rows kept per head
   int kv_parts;                         // splits of the queries of one key tile
-  size_t stat, range, tiles, part, total;
+  size_t stat, extra, range, tiles, part, total;
 };
 AttnBwdPlan attn_bwd_plan(const httm_attention& a);
 cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, cudaStream_t s);

@@ -3,16 +3,20 @@
 //   dV = P^T dO,  dP = dO V^T,  dS = P o (dP - D),  dQ = c dS K,  dK = c dS^T Q.
 //
 // Three launches (a fourth when key tiles are split):
-//  - attn_prep_kernel: -D and -lse * log2(e) of every query row, padded to
-//    whole tiles (rows outside the sequence or with an empty range get
-//    -infinity for the latter, so their P is 0 without a compare), and the
-//    key ranges of rows and of query tiles;
+//  - attn_prep_kernel: -D and -lse of every query row, padded to whole steps,
+//    as fp32 and as operands of three bf16 (see below), and the key ranges of
+//    rows and of steps;
 //  - attn_dkv_kernel: a CTA owns 128 keys and walks over the query tiles
 //    that see them, for all query heads sharing the key head; dK and dV stay
 //    in TMEM.  Everything is transposed (rows = keys): S^T = K Q^T and dP^T
 //    = V dO^T, so that P^T and dS^T are written back to TMEM as the A
 //    operands of dV += P^T dO and dK += dS^T Q, and nothing passes through
 //    shared memory but the loaded tiles;
+//    Here lse and D belong to a column, not to a thread's row: reading them
+//    from shared memory would cost 8 bytes an element of its bandwidth, as
+//    much as all else together (dK/dV 1087 us).  Instead one more K step of
+//    each product adds them: a row of ones times -lse / scale (-D) as the sum
+//    of three bf16, which holds an fp32 whole (XXX us);
 //  - attn_dq_kernel: a CTA owns 128 queries and walks over their keys; dS is
 //    the A operand of dQ += dS K.
 // Seven products a tile where one fused pass has five: dQ gathered from
@@ -68,10 +72,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kCols % kChunk == 0 && kCols % 16 == 0, "whole chunks, whole K steps");
 
 // ------------------------------------------------------------------ prep
+// x as the sum of three bf16 (24 bits: all of an fp32), and five zeros.
+__device__ __forceinline__ uint4 three_bf16(float x) {
+  const float hi = __bfloat162float(__float2bfloat16_rn(x)), mid = __bfloat162float(__float2bfloat16_rn(x - hi));
+  return make_uint4(pack_bf16(hi, mid), pack_bf16(x - hi - mid, 0.f), 0u, 0u);
+}
+
 // One step's 96 rows of one head a block, 8 threads a row.
 __global__ void __launch_bounds__(256)
 attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restrict__ nlse, float* __restrict__ ndsum,
-                 int2* __restrict__ ranges, AttnTileRange* __restrict__ tiles) {
+                 uint4* __restrict__ extra, int2* __restrict__ ranges, AttnTileRange* __restrict__ tiles) {
   __shared__ AttnTileRange part[8];
   const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, c = threadIdx.x & 7;
   const size_t Lp = (size_t)q_tiles * kStep;
@@ -97,8 +107,12 @@ attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restr
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (c == 0) {
-      nlse[bh * Lp + l] = live ? a.lse_in[(size_t)bh * a.L + l] * -kLog2e : -INFINITY;
+      const float lse = live ? a.lse_in[(size_t)bh * a.L + l] : 0.f;
+      nlse[bh * Lp + l] = live ? lse * -kLog2e : -INFINITY;
       ndsum[bh * Lp + l] = -s;
+      uint4* e = extra + ((size_t)bh * q_tiles + blockIdx.x) * 2 * kStep + (l - blockIdx.x * kStep);
+      e[0] = three_bf16(lse * (-1.f / a.scale));
+      e[kStep] = three_bf16(-s);
       if (h == 0) ranges[b * Lp + l] = keys;
     }
     if (live) {
@@ -134,11 +148,11 @@ attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restr
 // addresses in 16-byte units stay below the field's 14 bits).
 __device__ __forceinline__ uint64_t tile_desc(const uint8_t* tile) { return sw128_desc(smem_u32(tile), 1024); }
 
-// D = A B^T: K-major tiles of 128 and of 96 rows x 64 channels.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t A, uint64_t B) {
+// D (+)= A B^T: K-major tiles of 128 and of 96 rows x 64 channels.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t A, uint64_t B, bool add = false) {
   constexpr uint32_t id = idesc_bf16(128, kStep, false, false);
 #pragma unroll
-  for (int kk = 0; kk < kAttnD / 16; ++kk) umma_bf16(d, A + kk * 2, B + kk * 2, id, kk > 0);
+  for (int kk = 0; kk < kAttnD / 16; ++kk) umma_bf16(d, A + kk * 2, B + kk * 2, id, (add || kk > 0) ? 1u : 0u);
 }
 // D (+)= A B: A the 128 x 96 P or dS that the warpgroups of a group wrote to
 // the front of their columns of the product at `A`; B a tile of 96 rows x 64
@@ -151,12 +165,25 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, uint64_t B, boo
     umma_bf16_ts(d, A + (kk / per) * kCols + (kk % per) * 8, B + kk * 128, id, (add || kk > 0) ? 1u : 0u);
 }
 
-// Two neighbouring scores: s -> 2^(s c + m).
+// Two neighbouring scores: s -> 2^(s c + m), or 2^(s c).
 __device__ __forceinline__ void exp2_pair(uint32_t& s0, uint32_t& s1, unsigned long long cc, unsigned long long m) {
   float x0, x1;
   f2_unpack(f2_fma(f2_pack(__uint_as_float(s0), __uint_as_float(s1)), cc, m), x0, x1);
   s0 = __float_as_uint(ex2(x0));
   s1 = __float_as_uint(ex2(x1));
+}
+__device__ __forceinline__ void exp2_pair(uint32_t& s0, uint32_t& s1, unsigned long long cc) {
+  float x0, x1;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(s0), __uint_as_float(s1)), cc), x0, x1);
+  s0 = __float_as_uint(ex2(x0));
+  s1 = __float_as_uint(ex2(x1));
+}
+// Two neighbouring products, packed to bf16.
+__device__ __forceinline__ uint32_t mul_pair(uint32_t p0, uint32_t p1, uint32_t g0, uint32_t g1) {
+  float x0, x1;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(p0), __uint_as_float(p1)), f2_pack(__uint_as_float(g0), __uint_as_float(g1))),
+            x0, x1);
+  return pack_bf16(x0, x1);
 }
 // Two neighbouring p (dP + nd), packed to bf16.
 __device__ __forceinline__ uint32_t ds_pair(uint32_t p0, uint32_t p1, uint32_t g0, uint32_t g1, unsigned long long nd) {
@@ -170,7 +197,9 @@ __device__ __forceinline__ uint32_t ds_pair(uint32_t p0, uint32_t p1, uint32_t g
 struct DkvSmem {
   uint8_t k[kTileBytes], v[kTileBytes];
   uint8_t q[kStages][kStepBytes], g[kStages][kStepBytes];     // query and dout tiles
-  float nlse[kStages][kStep], ndsum[kStages][kStep];
+  uint4 ones[2][kAttnTile];                                   // K = 16 operand: 1 1 1 0 0 0 0 0, and zeros
+  uint4 extra[kStages][2][kStep];                             // its counterpart: -lse / scale, and -D
+  uint4 zeros[kStep];                                         // and the counterpart's other 8 columns
   int2 range[kStages][kStep];
   uint32_t active[kMaxWords], masked[kMaxWords], dead[kMaxWords];
   uint64_t kv_full, q_full[kStages], q_empty[kStages];
@@ -220,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
                 const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
                 const __grid_constant__ AttnArgs a, int q_tiles, int k_tiles, int parts,
-                const float* __restrict__ nlse, const float* __restrict__ ndsum, const int2* __restrict__ ranges,
+                const uint4* __restrict__ extra, const int2* __restrict__ ranges,
                 const AttnTileRange* __restrict__ tiles, float* __restrict__ part_out) {
   extern __shared__ uint8_t smem_raw[];
   DkvSmem& sm = *reinterpret_cast<DkvSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -254,6 +283,12 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
     mine += __popc(wa);
   }
   if (lane == 0) sm.count[warp] = mine;
+  for (int r = threadIdx.x; r < kAttnTile; r += kThreads) {
+    sm.ones[0][r] = make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u);
+    sm.ones[1][r] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < kStep) sm.zeros[r] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_async_smem();
   if (threadIdx.x == 0) {
     mbar_init(&sm.kv_full, 1);
     for (int s = 0; s < kStages; ++s) {
@@ -295,12 +330,10 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       for (int i = 0; i < n; ++i) {
         const int s = i % kStages, t = walk.next(), h = kh * a.G + walk.head;
         if (i >= kStages && !mbar_wait(&sm.q_empty[s], ((i / kStages) - 1) & 1, abort, st)) break;
-        const size_t at = ((size_t)b * a.H + h) * Lp + (size_t)t * kStep;
-        mbar_arrive_expect_tx(&sm.q_full[s], 2 * kStepBytes + kStep * 16);
+        mbar_arrive_expect_tx(&sm.q_full[s], 2 * kStepBytes + kStep * 40);
         tma_load_tile(sm.q[s], mq, &sm.q_full[s], t * kStep, h, b);
         tma_load_tile(sm.g[s], mg, &sm.q_full[s], t * kStep, h, b);
-        bulk_load(sm.nlse[s], nlse + at, kStep * 4, &sm.q_full[s]);
-        bulk_load(sm.ndsum[s], ndsum + at, kStep * 4, &sm.q_full[s]);
+        bulk_load(sm.extra[s], extra + (((size_t)b * a.H + h) * q_tiles + t) * 2 * kStep, kStep * 32, &sm.q_full[s]);
         bulk_load(sm.range[s], ranges + b * Lp + (size_t)t * kStep, kStep * 8, &sm.q_full[s]);
       }
     } else if ((warp == 1 || warp == 3) && n > 0) {
@@ -310,6 +343,10 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       const bool first = warp == 1;
       const uint64_t own = tile_desc(first ? sm.k : sm.v);
       const uint64_t rows = tile_desc(first ? sm.q[0] : sm.g[0]), cols = tile_desc(first ? sm.g[0] : sm.q[0]);
+      // one more K step adds -lse / scale to S and -D to dP
+      constexpr uint32_t id = idesc_bf16(128, kStep, false, false);
+      const uint64_t one = plain_desc(smem_u32(sm.ones), kAttnTile * 16, 128);
+      const uint32_t ext0 = smem_u32(sm.extra[0][first ? 0 : 1]), zeros = smem_u32(sm.zeros);
       const uint32_t buf = tmem + (first ? 0 : kStep), acc = tmem + (first ? kColA : kColB);
       uint64_t* full = first ? sm.s_full : sm.dp_full;
       uint64_t* ready = first ? sm.p_ready : sm.ds_ready;
@@ -324,9 +361,11 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         }
         tc_fence_after();
         const uint64_t desc = rows + s * (kStepBytes >> 4);
-        const uint32_t d = buf + grp * 2 * kStep;
+        const uint32_t d = buf + grp * 2 * kStep, ext = ext0 + s * (kStep * 32);
+        const uint64_t ed = plain_desc(ext, zeros - ext, 128);
         if (elect_one()) {
-          mma_rows(d, own, desc);
+          umma_bf16(d, one, ed, id, 0u);
+          mma_rows(d, own, desc, true);
           umma_commit(&full[grp]);
         }
         __syncwarp();
@@ -362,8 +401,8 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.dirty, n_dirty++ & 1, abort, st)) ||
             !__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)))
           break;
-        zero_rows(sm.q[s], kStep, [&](int r) { return sm.nlse[s][r] == -INFINITY; });
-        zero_rows(sm.g[s], kStep, [&](int r) { return sm.nlse[s][r] == -INFINITY; });
+        zero_rows(sm.q[s], kStep, [&](int r) { return sm.range[s][r].x >= sm.range[s][r].y; });
+        zero_rows(sm.g[s], kStep, [&](int r) { return sm.range[s][r].x >= sm.range[s][r].y; });
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.clean);
@@ -391,18 +430,13 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
           break;
         }
         tc_fence_after();
-        // p = 2^(s c - lse2) of this key and the queries of the columns
+        // p = 2^(c (s - lse / scale)) of this key and the queries of the columns
         uint32_t p[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
         tmem_wait_ld();
-        const ulonglong2* lp = reinterpret_cast<const ulonglong2*>(sm.nlse[s] + half * kCols);
 #pragma unroll
-        for (int e = 0; e < kCols / 4; ++e) {
-          const ulonglong2 x = lp[e];
-          exp2_pair(p[4 * e], p[4 * e + 1], cc, x.x);
-          exp2_pair(p[4 * e + 2], p[4 * e + 3], cc, x.y);
-        }
+        for (int e = 0; e < kCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc);
         if (masked) {
           const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + half * kCols);
 #pragma unroll
@@ -429,7 +463,6 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
           break;
         }
         tc_fence_after();
-        const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(sm.ndsum[s] + half * kCols);
 #pragma unroll
         for (int c = 0; c < kCols; c += kChunk) {
           uint32_t g[16], pk[8];
@@ -441,11 +474,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
               if (p[c + e] == 0u) g[e] = 0u;                    // a value nobody sees may be NaN
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const ulonglong2 x = dp[c / 4 + e];
-            pk[2 * e] = ds_pair(p[c + 4 * e], p[c + 4 * e + 1], g[4 * e], g[4 * e + 1], x.x);
-            pk[2 * e + 1] = ds_pair(p[c + 4 * e + 2], p[c + 4 * e + 3], g[4 * e + 2], g[4 * e + 3], x.y);
-          }
+          for (int e = 0; e < 8; ++e) pk[e] = mul_pair(p[c + 2 * e], p[c + 2 * e + 1], g[2 * e], g[2 * e + 1]);
           tmem_st8(td + c / 2, pk);
         }
         tmem_wait_st();
@@ -787,6 +816,7 @@ AttnBwdPlan attn_bwd_plan(const httm_attention& a) {
     return o;
   };
   p.stat = take((size_t)2 * a.batch * a.heads * p.Lp * sizeof(float));
+  p.extra = take((size_t)2 * a.batch * a.heads * p.Lp * 16);
   p.range = take((size_t)a.batch * p.Lp * sizeof(int2));
   p.tiles = take((size_t)a.batch * p.q_tiles * sizeof(AttnTileRange));
   p.part = take(p.kv_parts > 1 ? (size_t)items * p.kv_parts * 2 * kAttnTile * kAttnD * sizeof(float) : 0);
@@ -798,6 +828,7 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, c
   char* w = static_cast<char*>(ws);
   float* nlse = reinterpret_cast<float*>(w + p.stat);
   float* ndsum = nlse + (size_t)a.B * a.H * p.Lp;
+  uint4* extra = reinterpret_cast<uint4*>(w + p.extra);
   int2* ranges = reinterpret_cast<int2*>(w + p.range);
   AttnTileRange* tiles = reinterpret_cast<AttnTileRange*>(w + p.tiles);
   float* part = reinterpret_cast<float*>(w + p.part);
@@ -814,13 +845,13 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, c
       (e = cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem)) != cudaSuccess)
     return e;
   if (p.q_tiles > 0) {
-    attn_prep_kernel<<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, nlse, ndsum, ranges, tiles);
+    attn_prep_kernel<<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, nlse, ndsum, extra, ranges, tiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (p.k_tiles > 0) {
     const long long items = (long long)a.B * a.K * p.k_tiles;
     attn_dkv_kernel<<<(unsigned)(items * p.kv_parts), kThreads, kDkvSmem, s>>>(
-        mq, mg, mk, mv, a, p.q_tiles, p.k_tiles, p.kv_parts, nlse, ndsum, ranges, tiles, part);
+        mq, mg, mk, mv, a, p.q_tiles, p.k_tiles, p.kv_parts, extra, ranges, tiles, part);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.kv_parts > 1) {
       const long long rows = 2ll * a.B * a.K * a.N;

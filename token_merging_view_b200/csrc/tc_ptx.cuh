@@ -219,6 +219,18 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t sbo) {
   return d;
 }
 
+// The same for a K-major operand without swizzle: blocks of 8 rows x 16
+// bytes, stored as 128 consecutive bytes; `lbo` bytes from a block to the one
+// of the next 16 bytes of K, `sbo` to the one of the next 8 rows.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1u << 46;
+  return d;
+}
+
 // Instruction descriptor of kind::f16 with bf16 A/B, fp32 accumulate.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4)                                   // D format: f32
