@@ -201,6 +201,7 @@ struct DkvSmem {
   uint4 extra[kStages][2][kStep];                             // its counterpart: -lse / scale, and -D
   uint4 zeros[kStep];                                         // and the counterpart's other 8 columns
   int2 range[kStages][kStep];
+  int flags[kStages];                                         // kMasked, kDead of the step in each stage
   uint32_t active[kMaxWords], masked[kMaxWords], dead[kMaxWords];
   uint64_t kv_full, q_full[kStages], q_empty[kStages];
   uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2], drain, dirty, clean;
@@ -208,6 +209,7 @@ struct DkvSmem {
   uint32_t tmem_base;
   int abort;
 };
+constexpr int kMasked = 1, kDead = 2;
 constexpr size_t kDkvSmem = sizeof(DkvSmem) + 1024;
 static_assert(kDkvSmem <= 227 * 1024, "shared memory");
 static_assert(kStepBytes % 1024 == 0, "tiles start on 1024 bytes");
@@ -330,6 +332,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       for (int i = 0; i < n; ++i) {
         const int s = i % kStages, t = walk.next(), h = kh * a.G + walk.head;
         if (i >= kStages && !mbar_wait(&sm.q_empty[s], ((i / kStages) - 1) & 1, abort, st)) break;
+        sm.flags[s] = (sm.masked[t >> 5] >> (t & 31) & 1) * kMasked + (sm.dead[t >> 5] >> (t & 31) & 1) * kDead;
         mbar_arrive_expect_tx(&sm.q_full[s], 2 * kStepBytes + kStep * 40);
         tma_load_tile(sm.q[s], mq, &sm.q_full[s], t * kStep, h, b);
         tma_load_tile(sm.g[s], mg, &sm.q_full[s], t * kStep, h, b);
@@ -350,40 +353,57 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       const uint32_t buf = tmem + (first ? 0 : kStep), acc = tmem + (first ? kColA : kColB);
       uint64_t* full = first ? sm.s_full : sm.dp_full;
       uint64_t* ready = first ? sm.p_ready : sm.ds_ready;
-      TileWalk walk(sm.active, words, n_active, s0);
       int n_dirty = 0;
-      auto product = [&](int i) -> bool {
-        const int s = i % kStages, t = walk.next(), grp = i & 1;
+      // waits for the tiles of step i and clears rows that may hold anything
+      auto loaded = [&](int i) -> bool {
+        const int s = i % kStages;
         if (!wait_all(&sm.q_full[s], (i / kStages) & 1, abort, st)) return false;
-        if (__any_sync(0xffffffffu, sm.dead[t >> 5] >> (t & 31) & 1)) {   // rows that may hold anything
+        if (__any_sync(0xffffffffu, sm.flags[s] & kDead)) {
           if (lane == 0) mbar_arrive(&sm.dirty);
           if (!wait_all(&sm.clean, n_dirty++ & 1, abort, st)) return false;
         }
-        tc_fence_after();
-        const uint64_t desc = rows + s * (kStepBytes >> 4);
-        const uint32_t d = buf + grp * 2 * kStep, ext = ext0 + s * (kStep * 32);
-        const uint64_t ed = plain_desc(ext, zeros - ext, 128);
-        if (elect_one()) {
-          umma_bf16(d, one, ed, id, 0u);
-          mma_rows(d, own, desc, true);
-          umma_commit(&full[grp]);
-        }
-        __syncwarp();
         return true;
       };
-      bool ok = wait_all(&sm.kv_full, 0, abort, st) && product(0) && (n == 1 || product(1));
-      for (int i = 0; ok && i < n; ++i) {
-        const int s = i % kStages, grp = i & 1;
-        if (!wait_all(&ready[grp], (i >> 1) & 1, abort, st)) break;
+      // operands of product i (outside the elected branch: they stay uniform)
+      auto dest = [&](int i) { return buf + (i & 1) * 2 * kStep; };
+      auto row_desc = [&](int i) { return rows + (i % kStages) * (kStepBytes >> 4); };
+      auto ext_desc = [&](int i) {
+        const uint32_t ext = ext0 + (i % kStages) * (kStep * 32);
+        return plain_desc(ext, zeros - ext, 128);
+      };
+      bool ok = wait_all(&sm.kv_full, 0, abort, st);
+      for (int i = 0; ok && i < min(2, n); ++i) {
+        if (!(ok = loaded(i))) break;
         tc_fence_after();
-        const uint64_t desc = cols + s * (kStepBytes >> 4);
-        const uint32_t A = buf + grp * 2 * kStep;
+        const uint64_t rd = row_desc(i), ed = ext_desc(i);
+        const uint32_t d = dest(i);
         if (elect_one()) {
-          mma_cols(acc, A, desc, i > 0);
-          umma_commit(&sm.q_empty[s]);
+          umma_bf16(d, one, ed, id, 0u);
+          mma_rows(d, own, rd, true);
+          umma_commit(&full[i & 1]);
         }
         __syncwarp();
-        if (i + 2 < n) ok = product(i + 2);
+      }
+      // what the next product needs is waited for first, so that it follows
+      // the P (dS) it overwrites at once
+      for (int i = 0; ok && i < n; ++i) {
+        const int s = i % kStages, grp = i & 1;
+        const bool more = i + 2 < n;
+        if (more && !loaded(i + 2)) break;
+        const uint64_t rd = row_desc(i + 2), ed = ext_desc(i + 2), cd = cols + s * (kStepBytes >> 4);
+        const uint32_t d = dest(i);
+        if (!wait_all(&ready[grp], (i >> 1) & 1, abort, st)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_cols(acc, d, cd, i > 0);
+          umma_commit(&sm.q_empty[s]);
+          if (more) {
+            umma_bf16(d, one, ed, id, 0u);
+            mma_rows(d, own, rd, true);
+            umma_commit(&full[grp]);
+          }
+        }
+        __syncwarp();
       }
       if (elect_one()) {
         umma_commit(&sm.drain);                                 // every MMA ends before TMEM is released
@@ -418,18 +438,15 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
     const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2);
     bool ok = true;
     if (n > grp) {
-      TileWalk walk(sm.active, words, n_active, s0);
-      if (grp) walk.next();
       for (int i = grp; i < n; i += 2) {
-        const int s = i % kStages, t = walk.next(), m = i >> 1;
-        const bool masked = sm.masked[t >> 5] >> (t & 31) & 1;
-        if (i + 2 < n) walk.next();                             // the other group's
+        const int s = i % kStages, m = i >> 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) ||
             !__all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], m & 1, abort, st))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const bool masked = __any_sync(0xffffffffu, sm.flags[s] & kMasked);
         // p = 2^(c (s - lse / scale)) of this key and the queries of the columns
         uint32_t p[kCols];
 #pragma unroll
@@ -638,45 +655,53 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       const int g = warp >> 1;
       const uint64_t qd = tile_desc(sm.q), gd = tile_desc(sm.g), kd = tile_desc(sm.k[0]), vd = tile_desc(sm.v[0]);
       const uint32_t buf = tmem + g * 2 * kStep, acc = tmem + (g ? kColB : kColA);
-      auto issue_s = [&](int j) -> bool {
+      // waits for the tiles of step j; the last one's K rows behind the union are cleared
+      auto loaded = [&](int j) -> bool {
         const int s = j % kKvStages;
         if (!wait_all(&sm.kv_full[s], (j / kKvStages) & 1, abort, st)) return false;
         if (j == n - 1 && n_last < kStep) {
           if (lane == 0) mbar_arrive(&sm.dirty);
           if (!wait_all(&sm.clean, 0, abort, st)) return false;
         }
-        tc_fence_after();
-        const uint64_t desc = kd + s * (kStepBytes >> 4);
-        if (elect_one()) {
-          mma_rows(buf, qd, desc);
-          umma_commit(&sm.s_full[g]);
-        }
-        __syncwarp();
         return true;
       };
-      auto issue_dp = [&](int j) {
-        const uint64_t desc = vd + (j % kKvStages) * (kStepBytes >> 4);
+      bool ok = g < n && wait_all(&sm.q_full, 0, abort, st) && loaded(g);
+      if (ok) {
+        tc_fence_after();
+        const uint64_t k1 = kd + g * (kStepBytes >> 4), v1 = vd + g * (kStepBytes >> 4);
         if (elect_one()) {
-          mma_rows(buf + kStep, gd, desc);
+          mma_rows(buf, qd, k1);
+          umma_commit(&sm.s_full[g]);
+          mma_rows(buf + kStep, gd, v1);
           umma_commit(&sm.dp_full[g]);
         }
         __syncwarp();
-      };
-      bool ok = g < n && wait_all(&sm.q_full, 0, abort, st) && issue_s(g);
-      if (ok) issue_dp(g);
+      }
       for (int j = g; ok && j < n; j += 2) {
-        const int m = j >> 1, s = j % kKvStages;
-        if (!wait_all(&sm.s_read[g], m & 1, abort, st)) break;
-        if (j + 2 < n && !issue_s(j + 2)) break;
+        const int m = j >> 1, s = j % kKvStages, s2 = (j + 2) % kKvStages;
+        const bool more = j + 2 < n;
+        // operands outside the elected branches: they stay uniform
+        const uint64_t k0 = kd + s * (kStepBytes >> 4), k1 = kd + s2 * (kStepBytes >> 4), v1 = vd + s2 * (kStepBytes >> 4);
+        if (more) {
+          if (!wait_all(&sm.s_read[g], m & 1, abort, st) || !loaded(j + 2)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_rows(buf, qd, k1);
+            umma_commit(&sm.s_full[g]);
+          }
+          __syncwarp();
+        }
         if (!wait_all(&sm.ds_ready[g], m & 1, abort, st)) break;
         tc_fence_after();
-        const uint64_t desc = kd + s * (kStepBytes >> 4);
         if (elect_one()) {
-          mma_cols(acc, buf + kStep, desc, m > 0);
+          mma_cols(acc, buf + kStep, k0, m > 0);
           umma_commit(&sm.kv_empty[s]);
+          if (more) {
+            mma_rows(buf + kStep, gd, v1);                      // over the dS that dQ reads
+            umma_commit(&sm.dp_full[g]);
+          }
         }
         __syncwarp();
-        if (j + 2 < n) issue_dp(j + 2);                         // over the dS that dQ reads
       }
       if (elect_one()) {
         umma_commit(&sm.drain);                                 // every MMA ends before TMEM is released
