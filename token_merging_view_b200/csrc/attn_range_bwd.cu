@@ -51,7 +51,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kStages = 4;                            // query tiles in flight (dK, dV)
+constexpr int kStages = 5;                            // query tiles in flight (dK, dV)
 constexpr int kKvStages = 6;                          // key tiles in flight (dQ)
 constexpr int kStep = kAttnStep;
 constexpr int kHalves = 2;                            // warpgroups of a group
