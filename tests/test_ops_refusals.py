@@ -18,7 +18,7 @@ R = ctypes.byref
 
 def _cfg(**kw):
     a = dict(batch=2, heads=4, kv_heads=2, q_len=100, kv_len=300, d_head=64, dtype=0, softmax_scale=0.0,
-             key_begin=None, key_end=None)
+             key_begin=0, key_end=0)
     a.update(kw)
     return ops.httm_attention(*a.values())
 
@@ -32,7 +32,7 @@ def _view(heads, tokens, d=64, data=FAKE, **kw):
 def _forward(cfg=None, q=None, k=None, v=None, out=None, lse=FAKE, ws=FAKE, n=0, **kw):
     cfg = cfg or _cfg(**kw)
     views = [q or _view(4, 100), k or _view(2, 300), v or _view(2, 300), out or _view(4, 100)]
-    return B.load_library().httm_attention_forward(R(cfg), *map(R, views), lse, ws, n, None)
+    return B.load_library().httm_attention_forward(cfg, *views, lse, ws, n, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -45,15 +45,15 @@ def _forward(cfg=None, q=None, k=None, v=None, out=None, lse=FAKE, ws=FAKE, n=0,
 ])
 def test_attention_shapes(kw, status):
     assert _forward(**kw) == status
-    assert B.load_library().httm_attention_workspace_bytes(R(_cfg(**kw)), None, None) == status
+    assert B.load_library().httm_attention_workspace_bytes(_cfg(**kw), None, None) == status
 
 
 def test_attention_pointers_strides_and_workspace():
     lib = B.load_library()
     null = ctypes.c_void_p(None)
     assert lib.httm_attention_forward(None, null, null, null, null, None, None, 0, None) == ARG
-    assert lib.httm_attention_forward(R(_cfg()), null, null, null, null, None, None, 0, None) == ARG
-    assert _forward(q=_view(4, 100, data=None)) == ARG
+    assert lib.httm_attention_forward(_cfg(), null, null, null, null, None, None, 0, None) == ARG
+    assert _forward(q=_view(4, 100, data=0)) == ARG
     assert _forward(q=_view(4, 100, data=FAKE + 8)) == ALIGN
     assert _forward(k=_view(2, 300, token=68)) == ALIGN
     assert _forward(v=_view(2, 300, head=-64)) == ARG
@@ -72,13 +72,13 @@ def test_attention_pointers_strides_and_workspace():
     assert _forward(kv_len=8000, ws=FAKE + 16, n=need) == ALIGN
     # nothing to do
     assert _forward(batch=0) == 0
-    assert _forward(q_len=0, q=_view(4, 0, data=None), out=_view(4, 0, data=None)) == 0
+    assert _forward(q_len=0, q=_view(4, 0, data=0), out=_view(4, 0, data=0)) == 0
 
     def backward(ws=FAKE, n=0, lse=FAKE, **kw):
         q, k = _view(4, 100), _view(2, 300)
         views = [kw.get(x, y) for x, y in (("dout", q), ("q", q), ("k", k), ("v", k), ("out", q))]
         grads = [kw.get(x, y) for x, y in (("dq", q), ("dk", k), ("dv", k))]
-        return lib.httm_attention_backward(R(_cfg()), *map(R, views), lse, *map(R, grads), ws, n, None)
+        return lib.httm_attention_backward(_cfg(), *views, lse, *grads, ws, n, None)
 
     assert backward() == WORKSPACE
     assert backward(ws=None, n=1 << 40) == WORKSPACE
@@ -105,16 +105,16 @@ def _rot(**kw):
 
 def _rotary(q=None, q_out=None, k=None, k_out=None, **kw):
     views = [q or _view(4, 10), q_out or _view(4, 10), k or _view(2, 10), k_out or _view(2, 10)]
-    return B.load_library().httm_rotary(R(_rot(**kw)), *map(R, views), None)
+    return B.load_library().httm_rotary(_rot(**kw), *views, None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=-1), ARG), (dict(tokens=-1), ARG), (dict(heads=0), ARG), (dict(kv_heads=-1), ARG), (dict(d_head=0), ARG),
     (dict(axes=0), ARG), (dict(axes=5), ARG), (dict(pairs=0), ARG), (dict(pairs=17), ARG), (dict(layout=2), ARG),
-    (dict(dtype=2), ARG), (dict(factor=float("nan")), ARG), (dict(position_batch=-1), ARG), (dict(positions=None), ARG),
-    (dict(freqs=None), ARG), (dict(freqs=FAKE + 4), ALIGN), (dict(positions=FAKE + 2), ALIGN),
+    (dict(dtype=2), ARG), (dict(factor=float("nan")), ARG), (dict(position_batch=-1), ARG), (dict(positions=0), ARG),
+    (dict(freqs=0), ARG), (dict(freqs=FAKE + 4), ALIGN), (dict(positions=FAKE + 2), ALIGN),
     (dict(d_head=1025), UNSUPPORTED), (dict(tokens=0), 0), (dict(batch=0), 0),
-    (dict(q=ops.httm_view(FAKE + 1, 2560, 640, 64)), ALIGN), (dict(q=ops.httm_view(None, 2560, 640, 64)), ARG),
+    (dict(q=ops.httm_view(FAKE + 1, 2560, 640, 64)), ALIGN), (dict(q=ops.httm_view(0, 2560, 640, 64)), ARG),
     (dict(q_out=ops.httm_view(FAKE, 2560, 0, 64)), ARG), (dict(k=ops.httm_view(FAKE, -64, 640, 64)), ARG),
 ])
 def test_rotary_arguments(kw, status):
@@ -133,9 +133,9 @@ def _rows(data=FAKE, row=64):
 
 
 def _gated(x=None, f=True, y=True, z=True, gate=FAKE, w=None, **kw):
-    w = w or ops.httm_norm_weights(gate, None, None, None, None)
-    pick = lambda t: None if t is None else R(_rows()) if t is True else R(t)  # noqa: E731
-    return B.load_library().httm_gated_norm_forward(R(_norm(**kw)), R(w), R(x or _rows()), pick(f), pick(y), pick(z),
+    w = w or ops.httm_norm_weights(gate or 0, 0, 0, 0, 0)
+    pick = lambda t: _rows() if t is True else t  # noqa: E731
+    return B.load_library().httm_gated_norm_forward(_norm(**kw), w, x or _rows(), pick(f), pick(y), pick(z),
                                                     FAKE, None)
 
 
@@ -146,8 +146,8 @@ def _gated(x=None, f=True, y=True, z=True, gate=FAKE, w=None, **kw):
     (dict(gates=1025, rows=2050), UNSUPPORTED), (dict(rows=1 << 31, gates=1), UNSUPPORTED),
     (dict(branch_dtype=1), UNSUPPORTED), (dict(pre=0), ARG), (dict(z=None), ARG), (dict(gate=None), ARG),
     (dict(gates=0), ARG), (dict(f=None), ARG), (dict(y=None), ARG), (dict(f=None, y=None, gates=0, gate=None, residual_scale=2.0), ARG),
-    (dict(x=_rows(FAKE + 1)), ALIGN), (dict(x=_rows(None)), ARG), (dict(y=_rows(FAKE, 63)), ARG), (dict(z=_rows(FAKE, 0)), ARG),
-    (dict(w=ops.httm_norm_weights(FAKE, None, None, FAKE + 2, None)), ALIGN), (dict(rows=0), 0),
+    (dict(x=_rows(FAKE + 1)), ALIGN), (dict(x=_rows(0)), ARG), (dict(y=_rows(FAKE, 63)), ARG), (dict(z=_rows(FAKE, 0)), ARG),
+    (dict(w=ops.httm_norm_weights(FAKE, 0, 0, FAKE + 2, 0)), ALIGN), (dict(rows=0), 0),
 ])
 def test_gated_norm_arguments(kw, status):
     assert _gated(**kw) == status
@@ -158,24 +158,22 @@ def test_gated_norm_backward_arguments():
 
     def call(cfg=None, w=None, dy=_rows(), dz=_rows(), f=_rows(), y=_rows(), stats=FAKE, dx=_rows(), df=_rows(),
              grads=None, ws=None, n=0):
-        w = w or ops.httm_norm_weights(FAKE, None, None, None, None)
-        g = grads or ops.httm_norm_grads(FAKE, None, None, None, None)
-        p = lambda t: None if t is None else R(t)  # noqa: E731
-        return lib.httm_gated_norm_backward(R(cfg or _norm()), R(w), p(dy), p(dz), p(f), p(y), stats, p(dx), p(df), R(g),
-                                            ws, n, None)
+        w = w or ops.httm_norm_weights(FAKE, 0, 0, 0, 0)
+        g = grads or ops.httm_norm_grads(FAKE, 0, 0, 0, 0)
+        return lib.httm_gated_norm_backward(cfg or _norm(), w, dy, dz, f, y, stats, dx, df, g, ws, n, None)
 
     assert call() == WORKSPACE
     need = ctypes.c_size_t(0)
-    assert lib.httm_gated_norm_workspace_bytes(R(_norm()), R(need)) == 0 and need.value > 0
-    assert lib.httm_gated_norm_workspace_bytes(R(_norm()), None) == ARG
+    assert lib.httm_gated_norm_workspace_bytes(_norm(), R(need)) == 0 and need.value > 0
+    assert lib.httm_gated_norm_workspace_bytes(_norm(), None) == ARG
     assert call(ws=FAKE + 4, n=1 << 30) == ALIGN
     assert call(dz=None) == ARG
     assert call(y=None) == ARG
     assert call(stats=None) == ARG
     assert call(f=None) == ARG
-    assert call(grads=ops.httm_norm_grads(None, FAKE, None, None, None)) == ARG     # no post norm to have a gradient
+    assert call(grads=ops.httm_norm_grads(0, FAKE, 0, 0, 0)) == ARG     # no post norm to have a gradient
     assert call(dx=_rows(FAKE, 10)) == ARG
-    assert call(w=ops.httm_norm_weights(None, None, None, None, None)) == ARG
+    assert call(w=ops.httm_norm_weights(0, 0, 0, 0, 0)) == ARG
 
 
 def test_python_refuses_tensors_before_the_call():

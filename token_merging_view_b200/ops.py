@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 from dataclasses import dataclass
+from struct import Struct
 
 import torch
 
@@ -24,141 +25,150 @@ from .binding import HTTM_BF16, HTTM_F32, HttmError, _check, load_library  # noq
 HTTM_ROTARY_HALF, HTTM_ROTARY_PAIRS = 0, 1
 HTTM_NORM_NONE, HTTM_NORM_LAYER, HTTM_NORM_RMS = 0, 1, 2
 
-_I32, _I64, _F32, _PTR = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
-
-
-class httm_view(ctypes.Structure):
-    _fields_ = [("data", _PTR), ("batch", _I64), ("head", _I64), ("token", _I64)]
-
-
-class httm_attention(ctypes.Structure):
-    _fields_ = [(n, _I32) for n in ("batch", "heads", "kv_heads", "q_len", "kv_len", "d_head", "dtype")] + \
-        [("softmax_scale", _F32), ("key_begin", _PTR), ("key_end", _PTR)]
-
-
-class httm_rotary_cfg(ctypes.Structure):
-    _fields_ = [(n, _I32) for n in ("batch", "tokens", "heads", "kv_heads", "d_head", "dtype", "axes", "pairs",
-                                    "layout", "inverse")] + \
-        [("factor", _F32), ("positions", _PTR), ("position_batch", _I64), ("freqs", _PTR)]
-
-
-class httm_norm_cfg(ctypes.Structure):
-    _fields_ = [("rows", _I64)] + [(n, _I32) for n in ("channels", "stream_dtype", "branch_dtype", "post", "pre",
-                                                       "gates")] + \
-        [(n, _F32) for n in ("post_eps", "pre_eps", "residual_scale")]
-
-
-class httm_rows(ctypes.Structure):
-    _fields_ = [("data", _PTR), ("row", _I64)]
-
-
+_DTYPES = {torch.bfloat16: HTTM_BF16, torch.float32: HTTM_F32}
 _PARAMS = ("gate", "post_weight", "post_bias", "pre_weight", "pre_bias")
 
+# The C structs of include/httm.h as byte strings: small calls are bound by
+# the host, and packing one is several times cheaper than a ctypes.Structure.
+# Pointers are passed as integers (0: NULL); "0q" pads to a multiple of 8.
+httm_view = Struct("@P3q").pack             # data, batch, head, token strides
+httm_attention = Struct("@7if2P").pack      # batch .. dtype, softmax_scale, key_begin, key_end
+httm_rotary_cfg = Struct("@10ifPqP").pack   # batch .. inverse, factor, positions, position_batch, freqs
+httm_norm_cfg = Struct("@q6i3f0q").pack     # rows, channels .. gates, post_eps, pre_eps, residual_scale
+httm_rows = Struct("@Pq").pack              # data, row stride
+httm_norm_weights = httm_norm_grads = Struct("@5P").pack   # in the order of _PARAMS
 
-class httm_norm_weights(ctypes.Structure):
-    _fields_ = [(n, _PTR) for n in _PARAMS]
-
-
-class httm_norm_grads(ctypes.Structure):
-    _fields_ = [(n, _PTR) for n in _PARAMS]
-
-
-_DTYPES = {torch.bfloat16: HTTM_BF16, torch.float32: HTTM_F32}
-
-
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
+_device_of_thread = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _data(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-class _Call:
-    """One call's device and stream: every tensor must lie on that device."""
+def _common_device(named):
+    """The index of the one device all these tensors lie on."""
+    device, first = -1, None
+    grad = torch.is_grad_enabled()
+    for name, t in named:
+        if t is None:
+            continue
+        i = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if i < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device < 0:
+            device, first = i, name
+        elif i != device:
+            raise ValueError(f"{name} must be on the device of {first}, cuda:{device}")
+        if grad and t.requires_grad:
+            raise ValueError(f"{name} requires grad: this call records no graph (use torch.no_grad())")
+    return device
 
-    def __init__(self, stream, **tensors):
-        self.device = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            if self.device is None:
-                self.device = t.device
-            if t.device != self.device:
-                raise ValueError(f"{name} must be on {self.device}, like the other tensors")
-            if t.requires_grad and torch.is_grad_enabled():
-                raise ValueError(f"{name} requires grad: this call records no graph (use torch.no_grad())")
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream must belong to {self.device}")
-        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
-        self._ctx = torch.cuda.stream(self.stream)   # also makes its device the current one
+
+class _On:
+    """Makes the tensors' device (and `stream`, if given) the current one for
+    one call; yields the raw stream.  Costs nothing where both are already."""
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
 
     def __enter__(self):
-        self._ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        self.ctx = None
+        if self.stream is None and _device_of_thread() == self.device:
+            return _raw_stream(self.device)
+        stream = self.stream
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device.index != self.device:
+            raise ValueError(f"stream must belong to cuda:{self.device}")
+        self.ctx = torch.cuda.stream(stream)         # its device too
+        self.ctx.__enter__()
+        return stream.cuda_stream
 
     def __exit__(self, *a):
-        return self._ctx.__exit__(*a)
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
 
 
-def _heads(t, name):
-    """A [heads, tokens, d] or [batch, heads, tokens, d] tensor as 4-D."""
-    if t.dim() == 3:
-        t = t.unsqueeze(0)
-    if t.dim() != 4:
+def _view(t, name):
+    """The httm_view of a [heads, tokens, d] or [batch, heads, tokens, d] tensor."""
+    st = t.stride()
+    if len(st) == 3:
+        st = (0, *st)
+    elif len(st) != 4:
         raise ValueError(f"{name} must be [heads, tokens, d] or [batch, heads, tokens, d]")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if st[3] != 1 and t.shape[-1] > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    return t
+    return httm_view(t.data_ptr(), st[0], st[1], st[2])
 
 
-def _view(t):
-    return httm_view(_data(t), t.stride(0), t.stride(1), t.stride(2))
+def _heads_shape(t, name):
+    s = t.shape
+    if len(s) == 4:
+        return s
+    if len(s) == 3:
+        return (1, *s)
+    raise ValueError(f"{name} must be [heads, tokens, d] or [batch, heads, tokens, d]")
 
 
-def _same(t, like, name, dtype=None):
-    if tuple(t.shape) != tuple(like.shape) or t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{name} must be {dtype or like.dtype} {list(like.shape)}")
+def _new_like(t):
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _workspace(workspace, need, device):
+def _same(t, like, name):
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} {list(like.shape)}")
+
+
+def _workspace(workspace, need, like):
+    """(pointer, bytes, the tensor to keep alive through the call)."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
+        if need == 0:
+            return 0, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 # ------------------------------------------------------------------ attention
 def _attention(q, k, v, key_begin, key_end, softmax_scale):
-    q, k, v = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
-    B, H, L, d = q.shape
-    K, N = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != d or tuple(v.shape) != tuple(k.shape):
+    """The httm_attention of these tensors."""
+    B, H, L, d = _heads_shape(q, "q")
+    ks = _heads_shape(k, "k")
+    if ks[0] != B or ks[3] != d or v.shape != k.shape:
         raise ValueError("k and v must be [batch, kv_heads, kv_len, d] with q's batch and d")
-    if q.dtype not in _DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
+    dt = q.dtype
+    if dt not in _DTYPES or k.dtype != dt or v.dtype != dt:
         raise ValueError("q, k and v must have one type, bfloat16 (float32 is not supported by the kernels)")
     for name, t in (("key_begin", key_begin), ("key_end", key_end)):
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) not in ((B, L), (L,) if B == 1 else (B, L))
-                              or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or
+                              not (t.shape == (B, L) or (B == 1 and t.shape == (L,)))):
             raise ValueError(f"{name} must be a contiguous int32 [{B}, {L}] tensor")
-    cfg = httm_attention(B, H, K, L, N, d, _DTYPES[q.dtype], float(softmax_scale), _data(key_begin), _data(key_end))
-    return cfg, q, k, v
+    return httm_attention(B, H, ks[1], L, ks[2], d, _DTYPES[dt], softmax_scale, _data(key_begin), _data(key_end))
 
 
 def httm_attention_workspace_bytes(batch, heads, kv_heads, q_len, kv_len, d_head, dtype=torch.bfloat16):
     """(forward, backward) workspace bytes; no device call."""
-    cfg = httm_attention(batch, heads, kv_heads, q_len, kv_len, d_head, _DTYPES[dtype], 0.0, None, None)
-    return _attention_bytes(cfg)
+    return _attention_bytes(httm_attention(batch, heads, kv_heads, q_len, kv_len, d_head, _DTYPES[dtype], 0.0, 0, 0))
 
 
 def _attention_bytes(cfg):
-    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _check(load_library().httm_attention_workspace_bytes(_ref(cfg), _ref(f), _ref(b)),
-           "httm_attention_workspace_bytes")
-    return f.value, b.value
+    n = (ctypes.c_size_t * 2)()
+    st = load_library().httm_attention_workspace_bytes(cfg, ctypes.addressof(n), ctypes.addressof(n) + 8)
+    if st:
+        _check(st, "httm_attention_workspace_bytes")
+    return n[0], n[1]
+
+
+def _lse(lse, q):
+    shape = q.shape[:-1]
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=q.device)
+    if lse.shape != shape or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 {list(shape)} tensor")
+    return lse
 
 
 def httm_attention_forward(q, k, v, key_begin=None, key_end=None, softmax_scale=0.0, out=None, lse=None,
@@ -171,21 +181,20 @@ def httm_attention_forward(q, k, v, key_begin=None, key_end=None, softmax_scale=
     :func:`causal_ranges`, :func:`frame_ranges`, :func:`length_ranges`.
     softmax_scale 0 is 1 / sqrt(d).  Returns (out like q, lse float32
     [batch, heads, q_len])."""
-    call = _Call(stream, q=q, k=k, v=v, key_begin=key_begin, key_end=key_end, out=out, lse=lse, workspace=workspace)
-    with call as s:
-        cfg, q4, k4, v4 = _attention(q, k, v, key_begin, key_end, softmax_scale)
+    device = _common_device((("q", q), ("k", k), ("v", v), ("key_begin", key_begin), ("key_end", key_end),
+                             ("out", out), ("lse", lse), ("workspace", workspace)))
+    with _On(device, stream) as s:
+        cfg = _attention(q, k, v, key_begin, key_end, softmax_scale)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _same(out, q, "out")
-        if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-        _same(lse, q[..., 0], "lse", torch.float32)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-        ws = _workspace(workspace, _attention_bytes(cfg)[0], call.device)
-        vq, vk, vv, vo = _view(q4), _view(k4), _view(v4), _view(_heads(out, "out"))
-        _check(load_library().httm_attention_forward(_ref(cfg), _ref(vq), _ref(vk), _ref(vv), _ref(vo), _data(lse),
-                                                     _data(ws), ws.numel(), s), "httm_attention_forward")
+            out = _new_like(q)
+        else:
+            _same(out, q, "out")
+        lse = _lse(lse, q)
+        ws, n, keep = _workspace(workspace, _attention_bytes(cfg)[0], q)
+        st = load_library().httm_attention_forward(cfg, _view(q, "q"), _view(k, "k"), _view(v, "v"),
+                                                   _view(out, "out"), lse.data_ptr(), ws, n, s)
+        if st:
+            _check(st, "httm_attention_forward")
     return out, lse
 
 
@@ -194,24 +203,30 @@ def httm_attention_backward(dout, q, k, v, out, lse, key_begin=None, key_end=Non
     """The gradients (dq, dk, dv) of ``sum(dout * out)`` for the q, k, v,
     ranges and scale of a :func:`httm_attention_forward` call that returned
     (out, lse).  dk and dv add up the query heads that share a key head."""
-    call = _Call(stream, dout=dout, q=q, k=k, v=v, out=out, lse=lse, key_begin=key_begin, key_end=key_end, dq=dq,
-                 dk=dk, dv=dv, workspace=workspace)
-    with call as s:
-        cfg, q4, k4, v4 = _attention(q, k, v, key_begin, key_end, softmax_scale)
+    device = _common_device((("dout", dout), ("q", q), ("k", k), ("v", v), ("out", out), ("lse", lse),
+                             ("key_begin", key_begin), ("key_end", key_end), ("dq", dq), ("dk", dk), ("dv", dv),
+                             ("workspace", workspace)))
+    with _On(device, stream) as s:
+        cfg = _attention(q, k, v, key_begin, key_end, softmax_scale)
         _same(dout, q, "dout")
         _same(out, q, "out")
-        _same(lse, q[..., 0], "lse", torch.float32)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if g is None else g
-                      for g, t in ((dq, q), (dk, k), (dv, v)))
+        if lse is None:
+            raise ValueError("lse must be the forward call's")
+        lse = _lse(lse, q)
+        grads = []
         for name, g, t in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            _same(g, t, name)
-        ws = _workspace(workspace, _attention_bytes(cfg)[1], call.device)
-        views = [_view(_heads(t, n)) for t, n in ((dout, "dout"), (q4, "q"), (k4, "k"), (v4, "v"), (out, "out"))]
-        grads = [_view(_heads(t, n)) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv"))]
-        _check(load_library().httm_attention_backward(_ref(cfg), *map(_ref, views), _data(lse), *map(_ref, grads),
-                                                      _data(ws), ws.numel(), s), "httm_attention_backward")
+            if g is None:
+                g = _new_like(t)
+            else:
+                _same(g, t, name)
+            grads.append(g)
+        dq, dk, dv = grads
+        ws, n, keep = _workspace(workspace, _attention_bytes(cfg)[1], q)
+        st = load_library().httm_attention_backward(
+            cfg, _view(dout, "dout"), _view(q, "q"), _view(k, "k"), _view(v, "v"), _view(out, "out"), lse.data_ptr(),
+            _view(dq, "dq"), _view(dk, "dk"), _view(dv, "dv"), ws, n, s)
+        if st:
+            _check(st, "httm_attention_backward")
     return dq, dk, dv
 
 
@@ -279,35 +294,40 @@ def httm_rotary(q, k, freqs, positions, axes=1, layout=HTTM_ROTARY_HALF, factor=
     shared by the batch.  Outputs default to new contiguous tensors in the
     [batch, heads, tokens, d] order; q_out=q turns in place.  Returns (q_out,
     k_out)."""
-    call = _Call(stream, q=q, k=k, freqs=freqs, positions=positions, q_out=q_out, k_out=k_out)
-    with call as s:
-        q4 = _heads(q, "q")
-        B, H, T, d = q4.shape
-        if q.dtype not in _DTYPES:
+    device = _common_device((("q", q), ("k", k), ("freqs", freqs), ("positions", positions), ("q_out", q_out),
+                             ("k_out", k_out)))
+    with _On(device, stream) as s:
+        B, H, T, d = _heads_shape(q, "q")
+        dt = q.dtype
+        if dt not in _DTYPES:
             raise ValueError("q must be bfloat16 or float32")
-        k4 = None if k is None else _heads(k, "k")
-        if k4 is not None and (k4.shape[0] != B or k4.shape[2] != T or k4.shape[3] != d or k.dtype != q.dtype):
-            raise ValueError("k must have q's batch, tokens, channels and type")
         if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
             raise ValueError("freqs must be a contiguous float64 [pairs] tensor")
-        shapes = [(B, T, axes), (T, axes)] + ([(T,)] if axes == 1 else [])
-        if positions.dtype != torch.int32 or tuple(positions.shape) not in shapes or not positions.is_contiguous():
+        ps = positions.shape
+        if positions.dtype != torch.int32 or not positions.is_contiguous() or not (
+                ps == (B, T, axes) or ps == (T, axes) or (axes == 1 and ps == (T,))):
             raise ValueError(f"positions must be a contiguous int32 [{B}, {T}, {axes}] or [{T}, {axes}] tensor")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _same(q_out, q, "q_out")
+            q_out = _new_like(q)
+        else:
+            _same(q_out, q, "q_out")
+        kv_heads, vk, vk_out = 0, None, None
         if k is not None:
+            ks = _heads_shape(k, "k")
+            if ks[0] != B or ks[2] != T or ks[3] != d or k.dtype != dt:
+                raise ValueError("k must have q's batch, tokens, channels and type")
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            _same(k_out, k, "k_out")
+                k_out = _new_like(k)
+            else:
+                _same(k_out, k, "k_out")
+            kv_heads, vk, vk_out = ks[1], _view(k, "k"), _view(k_out, "k_out")
         elif k_out is not None:
             raise ValueError("k_out without k")
-        cfg = httm_rotary_cfg(B, T, H, 0 if k is None else k4.shape[1], d, _DTYPES[q.dtype], axes, freqs.numel(),
-                              layout, int(bool(inverse)), float(factor), _data(positions),
-                              T * axes if positions.dim() == 3 else 0, _data(freqs))
-        views = [_view(q4), _view(_heads(q_out, "q_out"))]
-        views += [None, None] if k is None else [_view(k4), _view(_heads(k_out, "k_out"))]
-        _check(load_library().httm_rotary(_ref(cfg), *map(_ref, views), s), "httm_rotary")
+        cfg = httm_rotary_cfg(B, T, H, kv_heads, d, _DTYPES[dt], axes, freqs.shape[0], layout, 1 if inverse else 0,
+                              factor, positions.data_ptr(), T * axes if len(ps) == 3 else 0, freqs.data_ptr())
+        st = load_library().httm_rotary(cfg, _view(q, "q"), _view(q_out, "q_out"), vk, vk_out, s)
+        if st:
+            _check(st, "httm_rotary")
     return q_out, k_out
 
 
@@ -325,44 +345,50 @@ _NO_NORM = Norm(HTTM_NORM_NONE)
 
 
 def _rows(t, shape, name, dtype):
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    if shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1:
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"the channels of {name} must be contiguous")
-    return httm_rows(_data(t), t.stride(0) if shape[0] > 1 else shape[1])
+    return httm_rows(t.data_ptr(), row if shape[0] > 1 else shape[1])
 
 
-def _norm_cfg(rows, channels, stream_dtype, branch_dtype, gate, post, pre, residual_scale):
-    for name, dt in (("stream", stream_dtype), ("branch", branch_dtype)):
-        if dt not in _DTYPES:
-            raise ValueError(f"the {name} must be bfloat16 or float32")
+def _norm_cfg(shape, stream_dtype, branch_dtype, gate, post, pre, residual_scale):
+    """(httm_norm_cfg, httm_norm_weights, the parameters in the order of _PARAMS)."""
+    if stream_dtype not in _DTYPES or branch_dtype not in _DTYPES:
+        raise ValueError("the stream and the branch must be bfloat16 or float32")
+    rows, channels = shape
     post, pre = post or _NO_NORM, pre or _NO_NORM
     gates = 0
     if gate is not None:
-        if gate.dim() == 1:
-            gate = gate.unsqueeze(0)
-        gates = gate.shape[0]
-        if gate.dim() != 2 or gate.shape[1] != channels or gates == 0:
+        gs = gate.shape
+        gates = gs[0] if len(gs) == 2 else 1
+        if gs[-1] != channels or len(gs) not in (1, 2) or gates == 0:
             raise ValueError(f"gate must be [{channels}] or [gates, {channels}]")
-    params = dict(zip(_PARAMS, (gate, post.weight, post.bias, pre.weight, pre.bias)))
-    for name, t in params.items():
+    params = (gate, post.weight, post.bias, pre.weight, pre.bias)
+    for name, t in zip(_PARAMS, params):
         if t is None:
             continue
         if t.dtype != torch.float32 or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32")
-        if name != "gate" and tuple(t.shape) != (channels,):
+        if t.shape != (channels,) and name != "gate":
             raise ValueError(f"{name} must be [{channels}]")
     cfg = httm_norm_cfg(rows, channels, _DTYPES[stream_dtype], _DTYPES[branch_dtype], post.kind, pre.kind, gates,
-                        post.eps, pre.eps, float(residual_scale))
-    return cfg, params, httm_norm_weights(*(_data(t) for t in params.values()))
+                        post.eps, pre.eps, residual_scale)
+    return cfg, httm_norm_weights(*map(_data, params)), params
 
 
-def _norm_tensors(gate, post, pre):
-    out = dict(gate=gate)
-    for side, n in (("post", post), ("pre", pre)):
-        if n is not None:
-            out[side + "_weight"], out[side + "_bias"] = n.weight, n.bias
-    return out
+def _norm_tensors(post, pre):
+    post, pre = post or _NO_NORM, pre or _NO_NORM
+    return (("post_weight", post.weight), ("post_bias", post.bias), ("pre_weight", pre.weight), ("pre_bias", pre.bias))
+
+
+def _stats(stats, rows, like):
+    if stats is None:
+        return torch.empty((4, rows), dtype=torch.float32, device=like.device)
+    if stats.dtype != torch.float32 or stats.shape != (4, rows) or not stats.is_contiguous():
+        raise ValueError(f"stats must be a contiguous float32 [4, {rows}] tensor")
+    return stats
 
 
 def httm_gated_norm_forward(x, f=None, gate=None, post=None, pre=None, residual_scale=1.0, y=None, z=None, stats=None,
@@ -376,30 +402,29 @@ def httm_gated_norm_forward(x, f=None, gate=None, post=None, pre=None, residual_
     z has f's type (without f: ``branch_dtype``, or x's).  y=x updates the
     stream in place.  Returns (y, z or None, stats float32 [4, rows] for the
     backward call)."""
-    call = _Call(stream, x=x, f=f, y=y, z=z, stats=stats, **_norm_tensors(gate, post, pre))
-    with call as s:
-        if x.dim() != 2:
+    device = _common_device((("x", x), ("f", f), ("gate", gate), ("y", y), ("z", z), ("stats", stats),
+                             *_norm_tensors(post, pre)))
+    with _On(device, stream) as s:
+        shape, xdt = x.shape, x.dtype
+        if len(shape) != 2:
             raise ValueError("x must be [rows, channels]")
-        shape = tuple(x.shape)
-        bdt = f.dtype if f is not None else branch_dtype or x.dtype
-        cfg, _, w = _norm_cfg(*shape, x.dtype, bdt, gate, post, pre, residual_scale)
+        bdt = f.dtype if f is not None else branch_dtype or xdt
+        cfg, weights, _ = _norm_cfg(shape, xdt, bdt, gate, post, pre, residual_scale)
         keep_x = f is None and y is None and residual_scale == 1.0 and pre is not None
         if y is None and not keep_x:
-            y = torch.empty(shape, dtype=x.dtype, device=x.device)
-        if pre is None and z is not None:
-            raise ValueError("z without pre")
-        if pre is not None and z is None:
+            y = _new_like(x)
+        if pre is None:
+            if z is not None:
+                raise ValueError("z without pre")
+        elif z is None:
             z = torch.empty(shape, dtype=bdt, device=x.device)
-        if stats is None:
-            stats = torch.empty((4, shape[0]), dtype=torch.float32, device=x.device)
-        if stats.dtype != torch.float32 or tuple(stats.shape) != (4, shape[0]) or not stats.is_contiguous():
-            raise ValueError(f"stats must be a contiguous float32 [4, {shape[0]}] tensor")
-        rx = _rows(x, shape, "x", x.dtype)
-        rf = None if f is None else _rows(f, shape, "f", bdt)
-        ry = None if y is None else _rows(y, shape, "y", x.dtype)
-        rz = None if z is None else _rows(z, shape, "z", bdt)
-        _check(load_library().httm_gated_norm_forward(_ref(cfg), _ref(w), _ref(rx), _ref(rf), _ref(ry), _ref(rz),
-                                                      _data(stats), s), "httm_gated_norm_forward")
+        stats = _stats(stats, shape[0], x)
+        st = load_library().httm_gated_norm_forward(
+            cfg, weights, _rows(x, shape, "x", xdt), None if f is None else _rows(f, shape, "f", bdt),
+            None if y is None else _rows(y, shape, "y", xdt), None if z is None else _rows(z, shape, "z", bdt),
+            stats.data_ptr(), s)
+        if st:
+            _check(st, "httm_gated_norm_forward")
     return (x if keep_x else y), z, stats
 
 
@@ -410,49 +435,55 @@ def httm_gated_norm_backward(dy, dz, f, y, stats, gate=None, post=None, pre=None
     scale that returned (y, z, stats).  dy may be None (0).  Returns a dict:
     dx, df, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias; None
     where the forward call had no such input."""
-    call = _Call(stream, dy=dy, dz=dz, f=f, y=y, stats=stats, dx=dx, df=df, workspace=workspace,
-                 **_norm_tensors(gate, post, pre))
-    with call as s:
-        if y.dim() != 2:
+    device = _common_device((("dy", dy), ("dz", dz), ("f", f), ("y", y), ("stats", stats), ("gate", gate), ("dx", dx),
+                             ("df", df), ("workspace", workspace), *_norm_tensors(post, pre)))
+    with _On(device, stream) as s:
+        shape, sdt = y.shape, y.dtype
+        if len(shape) != 2:
             raise ValueError("y must be [rows, channels]")
         if (dz is None) != (pre is None):
             raise ValueError("dz must be given exactly when pre is")
-        shape = tuple(y.shape)
-        bdt = f.dtype if f is not None else dz.dtype if dz is not None else y.dtype
-        cfg, params, w = _norm_cfg(*shape, y.dtype, bdt, gate, post, pre, residual_scale)
-        if stats.dtype != torch.float32 or tuple(stats.shape) != (4, shape[0]) or not stats.is_contiguous():
-            raise ValueError(f"stats must be a contiguous float32 [4, {shape[0]}] tensor")
+        if stats is None:
+            raise ValueError("stats must be the forward call's")
+        bdt = f.dtype if f is not None else dz.dtype if dz is not None else sdt
+        cfg, weights, params = _norm_cfg(shape, sdt, bdt, gate, post, pre, residual_scale)
+        stats = _stats(stats, shape[0], y)
         if dx is None:
-            dx = torch.empty(shape, dtype=y.dtype, device=y.device)
-        if f is None and df is not None:
-            raise ValueError("df without f")
-        if f is not None and df is None:
-            df = torch.empty(shape, dtype=bdt, device=y.device)
-        grads = {n: None if t is None else torch.empty_like(t) for n, t in params.items()}
-        g = httm_norm_grads(*(_data(t) for t in grads.values()))
+            dx = _new_like(y)
+        if f is None:
+            if df is not None:
+                raise ValueError("df without f")
+        elif df is None:
+            df = _new_like(f)
+        # all parameter gradients in one allocation
+        sizes = [0 if t is None else t.numel() for t in params]
+        flat = torch.empty(sum(sizes), dtype=torch.float32, device=y.device) if any(sizes) else None
+        grads, at = [], 0
+        for t, n in zip(params, sizes):
+            grads.append(None if t is None else flat[at:at + n] if t.dim() == 1 else flat[at:at + n].view(t.shape))
+            at += n
         need = ctypes.c_size_t(0)
-        _check(load_library().httm_gated_norm_workspace_bytes(_ref(cfg), _ref(need)), "httm_gated_norm_workspace_bytes")
-        ws = _workspace(workspace, need.value if any(t is not None for t in grads.values()) else 0, call.device)
-        sdt = y.dtype
-        rows = [None if t is None else _rows(t, shape, n, dt) for t, n, dt in
-                ((dy, "dy", sdt), (dz, "dz", bdt), (f, "f", bdt), (y, "y", sdt))]
-        outs = [None if t is None else _rows(t, shape, n, dt) for t, n, dt in ((dx, "dx", sdt), (df, "df", bdt))]
-        _check(load_library().httm_gated_norm_backward(_ref(cfg), _ref(w), *map(_ref, rows), _data(stats),
-                                                       *map(_ref, outs), _ref(g), _data(ws), ws.numel(), s),
-               "httm_gated_norm_backward")
-        if gate is not None and gate.dim() == 1:
-            grads["gate"] = grads["gate"][0]
-    return dict(dx=dx, df=df, **{"d" + n: t for n, t in grads.items()})
+        lib = load_library()
+        st = lib.httm_gated_norm_workspace_bytes(cfg, ctypes.addressof(need))
+        if st:
+            _check(st, "httm_gated_norm_workspace_bytes")
+        ws, n, keep = _workspace(workspace, need.value if flat is not None else 0, y)
+        rows = [None if t is None else _rows(t, shape, name, dt) for name, t, dt in
+                (("dy", dy, sdt), ("dz", dz, bdt), ("f", f, bdt), ("y", y, sdt), ("dx", dx, sdt), ("df", df, bdt))]
+        st = lib.httm_gated_norm_backward(cfg, weights, *rows[:4], stats.data_ptr(), *rows[4:],
+                                          httm_norm_grads(*map(_data, grads)), ws, n, s)
+        if st:
+            _check(st, "httm_gated_norm_backward")
+    return dict(dx=dx, df=df, **{"d" + name: t for name, t in zip(_PARAMS, grads)})
 
 
 def httm_ops_device_status(device=None, stream=None) -> int:
     """Synchronises the stream; returns the HTTM_DEV_* bits the operators'
     kernels set on the device since the last call (0 = clean)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
     v = ctypes.c_uint32(0)
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        st = load_library().httm_ops_device_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(v))
+    with _On(index, stream) as s:
+        st = load_library().httm_ops_device_status(s, ctypes.byref(v))
     if st not in (0, 7, 8):
         _check(st, "httm_ops_device_status")
     return int(v.value)
