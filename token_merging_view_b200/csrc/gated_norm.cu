@@ -45,70 +45,116 @@ struct NormArgs {
 };
 enum { kGate = 0, kPostW, kPostB, kPreW, kPreB, kNumGrads };
 
-template <class T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+// E neighbouring elements, 4 or 8, as raw words: bf16 pairs or fp32.
+template <class T, int E>
+struct Words {
+  static constexpr int n = E * (int)sizeof(T) / 4;
+  uint32_t w[n];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (n == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      for (int i = 0; i < n / 4; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
     }
   }
-}
-template <class T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint32_t u[4];
+  __device__ __forceinline__ void get(float (&v)[E]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int e = 0; e < E; ++e) {
+      if constexpr (sizeof(T) == 4) v[e] = __uint_as_float(w[e]);
+      else v[e] = __uint_as_float((e & 1) ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
   }
-}
+  __device__ __forceinline__ void set(const float (&v)[E]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = __float_as_uint(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (n == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < n / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+};
 
-// The channels of a thread.  VEC: vector v covers 8 neighbouring channels,
-// in 16-byte accesses (channels a multiple of 8, rows aligned); else the 8
-// are NT apart, so that neighbouring threads touch neighbouring elements.
-template <int NT, bool VEC>
+// The channels of a thread.  VEC: vector v covers E neighbouring channels,
+// in one or two wide accesses (channels a multiple of 8, rows aligned); else
+// the E are NT apart, so that neighbouring threads touch neighbouring
+// elements.
+template <int NT, bool VEC, int E = 8>
 struct Cols {
   int t, C;
-  __device__ __forceinline__ int at(int v, int e) const { return VEC ? (v * NT + t) * 8 + e : (v * 8 + e) * NT + t; }
+  __device__ __forceinline__ int at(int v, int e) const { return VEC ? (v * NT + t) * E + e : (v * E + e) * NT + t; }
   __device__ __forceinline__ bool live(int v, int e) const { return at(v, VEC ? 0 : e) < C; }
-  // elements behind the row's end read as `fill`
+  // elements behind the row's end read as 0
   template <class T>
-  __device__ __forceinline__ void load(const T* row, int v, float (&r)[8], float fill = 0.f) const {
+  __device__ __forceinline__ void load(const T* row, int v, float (&r)[E]) const {
     if constexpr (VEC) {
       if (live(v, 0)) {
-        load8(row + at(v, 0), r);
+        Words<T, E> w;
+        w.load(row + at(v, 0));
+        w.get(r);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = fill;
+        for (int e = 0; e < E; ++e) r[e] = 0.f;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = live(v, e) ? to_f(row[at(v, e)]) : fill;
+      for (int e = 0; e < E; ++e) r[e] = live(v, e) ? to_f(row[at(v, e)]) : 0.f;
     }
   }
   template <class T>
-  __device__ __forceinline__ void store(T* row, int v, const float (&r)[8]) const {
+  __device__ __forceinline__ void store(T* row, int v, const float (&r)[E]) const {
     if constexpr (VEC) {
-      if (live(v, 0)) store8(row + at(v, 0), r);
+      if (live(v, 0)) {
+        Words<T, E> w;
+        w.set(r);
+        w.store(row + at(v, 0));
+      }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < E; ++e)
         if (live(v, e)) row[at(v, e)] = from_f<T>(r[e]);
     }
   }
+};
+
+// A row's E channels of a thread as loaded, converted when they are used: a
+// row in flight costs few registers.
+template <class T, int NT, bool VEC, int E>
+struct Raw {
+  using W = std::conditional_t<VEC, Words<T, E>, Words<float, E>>;
+  W words;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < W::n; ++i) words.w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const Cols<NT, VEC, E>& cols, const void* base, int64_t row, int64_t stride) {
+    const T* p = static_cast<const T*>(base) + row * stride;
+    if constexpr (VEC) {
+      if (cols.live(0, 0)) words.load(p + cols.at(0, 0));
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (cols.live(0, e)) words.w[e] = __float_as_uint(to_f(p[cols.at(0, e)]));
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[E]) const { words.get(v); }
 };
 
 // Sum over the NT threads of a row (all of them get it).  NT = 32: shuffles;
@@ -239,99 +285,148 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs
   }
 }
 
+// Backward: channels a thread, threads a row, and the blocks an SM is to
+// hold.  With 4 channels the sums and the row in flight fit 80 registers (24
+// warps an SM); rows of over 4,096 channels take 8.
+constexpr int grad_channels(int C) { return C <= 4096 ? 4 : 8; }
+constexpr int grad_threads(int C) {
+  int nt = 32;
+  while (nt * grad_channels(C) < C) nt *= 2;
+  return nt;
+}
+constexpr int grad_blocks(int NT, int E) { return E == 8 || NT == 1024 ? 1 : 768 / (NT > 32 ? NT : 128); }
+
 // Backward: thread group g of gate group q walks over its share of that
-// group's rows with 8 channels a thread.
-template <class TX, class TF, int NT, bool VEC>
-__global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_grad_kernel(NormArgs a) {
+// group's rows with E channels a thread, one row ahead with its loads.  POST:
+// there is a norm on the block's output (two more parameter gradients and
+// another pair of sums a row).
+template <class TX, class TF, int NT, bool VEC, bool POST, int E>
+__global__ void __launch_bounds__(NT > 32 ? NT : 128, grad_blocks(NT, E))
+gated_norm_grad_kernel(NormArgs a) {
   constexpr int kGroups = NT > 32 ? 1 : 4;                    // thread groups per block (barriers need one)
   __shared__ float tmp[2][2][32];
   int turn = 0;
   const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / NT;
   const int n_gates = max(1, a.gates);
   if (group >= (int64_t)n_gates * a.chunks) return;
-  const Cols<NT, VEC> cols{(int)(threadIdx.x % NT), a.C};
+  const Cols<NT, VEC, E> cols{(int)(threadIdx.x % NT), a.C};
   const float inv_c = 1.f / (float)a.C;
   const int gq = (int)(group / a.chunks), chunk = (int)(group % a.chunks);
   const int64_t r0 = gq * a.gate_rows + a.gate_rows * chunk / a.chunks;
   const int64_t r1 = gq * a.gate_rows + a.gate_rows * (chunk + 1) / a.chunks;
+  const bool pre = a.pre != HTTM_NORM_NONE;
 
-  float gate[8], post_w[8], pre_w[8], post_b[8];
+  float gate[E], pre_w[E], post_w[POST ? E : 1], post_b[POST ? E : 1];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) gate[e] = post_w[e] = pre_w[e] = 1.f, post_b[e] = 0.f;
+  for (int e = 0; e < E; ++e) gate[e] = pre_w[e] = 1.f;
   if (a.gate) cols.load(a.gate + (int64_t)gq * a.C, 0, gate);
-  if (a.post_w) cols.load(a.post_w, 0, post_w);
-  if (a.post_b) cols.load(a.post_b, 0, post_b);
   if (a.pre_w) cols.load(a.pre_w, 0, pre_w);
-  float acc[kNumGrads][8];
+  if constexpr (POST) {
 #pragma unroll
-  for (int k = 0; k < kNumGrads; ++k)
+    for (int e = 0; e < E; ++e) post_w[e] = 1.f, post_b[e] = 0.f;
+    if (a.post_w) cols.load(a.post_w, 0, post_w);
+    if (a.post_b) cols.load(a.post_b, 0, post_b);
+  }
+  constexpr int kAcc = POST ? 5 : 3;
+  enum { aGate = 0, aPreW, aPreB, aPostW, aPostB };
+  float acc[kAcc][E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+  for (int k = 0; k < kAcc; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
 
+  Raw<TX, NT, VEC, E> next_dy, next_y;
+  Raw<TF, NT, VEC, E> next_f, next_dz;
+  next_dy.clear();
+  next_y.clear();
+  next_f.clear();
+  next_dz.clear();
+  float pre_mean = 0.f, pre_r = 0.f, post_mean = 0.f, post_r = 0.f;
+  auto fetch = [&](int64_t row) {
+    if (a.dy) next_dy.load(cols, a.dy, row, a.sdy);
+    if (a.f) next_f.load(cols, a.f, row, a.sf);
+    if (pre) {
+      next_y.load(cols, a.y, row, a.sy);
+      next_dz.load(cols, a.dz, row, a.sdz);
+      pre_mean = a.pre == HTTM_NORM_LAYER ? a.stats[2 * a.rows + row] : 0.f;
+      pre_r = a.stats[3 * a.rows + row];
+    }
+    if constexpr (POST) {
+      post_mean = a.post == HTTM_NORM_LAYER ? a.stats[row] : 0.f;
+      post_r = a.stats[a.rows + row];
+    }
+  };
+  if (r0 < r1) fetch(r0);
   for (int64_t row = r0; row < r1; ++row) {
-    float g[8], f[8], y[8], dz[8];
+    float g[E], f[E], y[E], dz[E];
+    next_dy.get(g);
+    next_f.get(f);
+    next_y.get(y);
+    next_dz.get(dz);
+    const float m_pre = pre_mean, r_pre = pre_r, m_post = post_mean, r_post = post_r;
+    if (row + 1 < r1) fetch(row + 1);
+    if (pre) {
+      float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = f[e] = 0.f;
-    if (a.dy) cols.load(static_cast<const TX*>(a.dy) + row * a.sdy, 0, g);
-    if (a.f) cols.load(static_cast<const TF*>(a.f) + row * a.sf, 0, f);
-    if (a.pre != HTTM_NORM_NONE) {
-      cols.load(static_cast<const TX*>(a.y) + row * a.sy, 0, y);
-      cols.load(static_cast<const TF*>(a.dz) + row * a.sdz, 0, dz);
-      const float mean = a.pre == HTTM_NORM_LAYER ? a.stats[2 * a.rows + row] : 0.f, r = a.stats[3 * a.rows + row];
-      float s[2] = {0.f, 0.f}, u[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = cols.live(0, e) ? (y[e] - mean) * r : 0.f;
-        u[e] = dz[e] * pre_w[e];
-        s[0] += u[e];
-        s[1] = fmaf(u[e], y[e], s[1]);
-        acc[kPreW][e] = fmaf(dz[e], y[e], acc[kPreW][e]);
-        acc[kPreB][e] += dz[e];
+      for (int e = 0; e < E; ++e) {
+        y[e] = cols.live(0, e) ? (y[e] - m_pre) * r_pre : 0.f;
+        acc[aPreW][e] = fmaf(dz[e], y[e], acc[aPreW][e]);
+        acc[aPreB][e] += dz[e];
+        dz[e] *= pre_w[e];
+        s[0] += dz[e];
+        s[1] = fmaf(dz[e], y[e], s[1]);
       }
       row_sums<NT, 2>(s, tmp, turn);
       const float m0 = a.pre == HTTM_NORM_LAYER ? s[0] * inv_c : 0.f, m1 = s[1] * inv_c;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = fmaf(r, u[e] - m0 - y[e] * m1, g[e]);
+      for (int e = 0; e < E; ++e) g[e] = fmaf(r_pre, dz[e] - m0 - y[e] * m1, g[e]);
     }
     if (a.dx) {
-      float o[8];
+      float o[E];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = a.rs * g[e];
+      for (int e = 0; e < E; ++e) o[e] = a.rs * g[e];
       cols.store(static_cast<TX*>(a.dx) + row * a.sdx, 0, o);
     }
     if (a.f) {
-      if (a.post == HTTM_NORM_NONE) {
+      if constexpr (!POST) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          acc[kGate][e] = fmaf(g[e], f[e], acc[kGate][e]);
+        for (int e = 0; e < E; ++e) {
+          acc[aGate][e] = fmaf(g[e], f[e], acc[aGate][e]);
           g[e] *= gate[e];
         }
       } else {
-        const float mean = a.post == HTTM_NORM_LAYER ? a.stats[row] : 0.f, r = a.stats[a.rows + row];
-        float s[2] = {0.f, 0.f}, u[8];
+        float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] = cols.live(0, e) ? (f[e] - mean) * r : 0.f;
-          acc[kGate][e] = fmaf(g[e], fmaf(f[e], post_w[e], post_b[e]), acc[kGate][e]);
+        for (int e = 0; e < E; ++e) {
+          f[e] = cols.live(0, e) ? (f[e] - m_post) * r_post : 0.f;
+          acc[aGate][e] = fmaf(g[e], fmaf(f[e], post_w[e], post_b[e]), acc[aGate][e]);
           g[e] *= gate[e];
-          acc[kPostW][e] = fmaf(g[e], f[e], acc[kPostW][e]);
-          acc[kPostB][e] += g[e];
-          u[e] = g[e] * post_w[e];
-          s[0] += u[e];
-          s[1] = fmaf(u[e], f[e], s[1]);
+          acc[aPostW][e] = fmaf(g[e], f[e], acc[aPostW][e]);
+          acc[aPostB][e] += g[e];
+          g[e] *= post_w[e];
+          s[0] += g[e];
+          s[1] = fmaf(g[e], f[e], s[1]);
         }
         row_sums<NT, 2>(s, tmp, turn);
         const float m0 = a.post == HTTM_NORM_LAYER ? s[0] * inv_c : 0.f, m1 = s[1] * inv_c;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = r * (u[e] - m0 - f[e] * m1);
+        for (int e = 0; e < E; ++e) g[e] = r_post * (g[e] - m0 - f[e] * m1);
       }
       if (a.df) cols.store(static_cast<TF*>(a.df) + row * a.sdf, 0, g);
     }
   }
+  // partial sums in the order of kGate .. kPreB, wanted ones only
   const int64_t n_part = (int64_t)n_gates * a.chunks;
-#pragma unroll
-  for (int k = 0; k < kNumGrads; ++k)
-    if (a.want >> k & 1) cols.store(a.partial + ((int64_t)__popc(a.want & ((1u << k) - 1)) * n_part + group) * a.C, 0, acc[k]);
+  auto put = [&](int k, const float (&v)[E]) {
+    if (a.want >> k & 1) cols.store(a.partial + ((int64_t)__popc(a.want & ((1u << k) - 1)) * n_part + group) * a.C, 0, v);
+  };
+  put(kGate, acc[aGate]);
+  put(kPreW, acc[aPreW]);
+  put(kPreB, acc[aPreB]);
+  if constexpr (POST) {
+    put(kPostW, acc[aPostW]);
+    put(kPostB, acc[aPostB]);
+  }
 }
 
 struct SumArgs {
@@ -341,11 +436,11 @@ struct SumArgs {
   int C, gates, chunks;
 };
 
-// Adds up the partial rows: 32 channels a block, 32 threads down the rows,
-// each in order, then the 32 in order.
+// Adds up the partial rows: 16 channels a block, 64 threads down the rows,
+// each in order, then the 64 in order.
 __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
-  __shared__ float s[32][33];
-  const int k = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float s[64][17];
+  const int k = blockIdx.y, col = blockIdx.x * 16 + threadIdx.x;
   const bool per_gate = k == 0 && a.is_gate0;
   const int64_t n_part = (int64_t)a.gates * a.chunks;
   const int64_t p0 = per_gate ? (int64_t)blockIdx.z * a.chunks : 0, n = per_gate ? a.chunks : n_part;
@@ -353,29 +448,26 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
   float v = 0.f;
   if (col < a.C) {
     const float* p = a.partial + ((int64_t)k * n_part + p0) * a.C + col;
-#pragma unroll 4
-    for (int64_t i = threadIdx.y; i < n; i += 32) v += p[i * a.C];
+#pragma unroll 8
+    for (int64_t i = threadIdx.y; i < n; i += 64) v += p[i * a.C];
   }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y == 0 && col < a.C) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    for (int i = 0; i < 64; ++i) t += s[i][threadIdx.x];
     a.out[k][(per_gate ? (int64_t)blockIdx.z * a.C : 0) + col] = t;
   }
 }
 
-// Thread groups per gate group of the backward kernel: enough groups to
-// fill the SMs (about 512 threads each), at least 4 rows each.
-int grad_threads(int C) {
-  int nt = 32;
-  while (nt * 8 < C) nt *= 2;
-  return nt;
-}
+// Thread groups per gate group of the backward kernel: as many as the SMs
+// hold at once, at least 4 rows a group.
 int grad_chunks(const httm_norm_cfg& c) {
   const int64_t gates = std::max(1, c.gates), rows = c.rows / gates;
-  const int64_t want = std::max<int64_t>(1, (int64_t)kSMs * 512 / grad_threads(c.channels) / gates);
+  const int nt = grad_threads(c.channels);
+  const int64_t per_sm = grad_blocks(nt, grad_channels(c.channels)) * (nt > 32 ? 1 : 4);
+  const int64_t want = std::max<int64_t>(1, kSMs * per_sm / gates);
   return (int)std::max<int64_t>(1, std::min(want, rows / 4));
 }
 
@@ -397,21 +489,22 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <class TX, class TF, bool VEC>
+template <class TX, class TF, bool VEC, bool POST>
 cudaError_t launch_grad(const NormArgs& a, cudaStream_t s) {
-#define HTTM_NORM_BWD(NT)                                                                          \
-  do {                                                                                             \
-    constexpr int kGroups = (NT) > 32 ? 1 : 4;                                                     \
-    const int64_t grid = ((int64_t)std::max(1, a.gates) * a.chunks + kGroups - 1) / kGroups;       \
-    gated_norm_grad_kernel<TX, TF, NT, VEC><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a);  \
+#define HTTM_NORM_BWD(NT, E)                                                                          \
+  do {                                                                                                \
+    constexpr int kGroups = (NT) > 32 ? 1 : 4;                                                        \
+    const int64_t grid = ((int64_t)std::max(1, a.gates) * a.chunks + kGroups - 1) / kGroups;          \
+    gated_norm_grad_kernel<TX, TF, NT, VEC, POST, E><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a); \
   } while (0)
-  switch (grad_threads(a.C)) {
-    case 32: HTTM_NORM_BWD(32); break;
-    case 64: HTTM_NORM_BWD(64); break;
-    case 128: HTTM_NORM_BWD(128); break;
-    case 256: HTTM_NORM_BWD(256); break;
-    case 512: HTTM_NORM_BWD(512); break;
-    default: HTTM_NORM_BWD(1024); break;
+  if (grad_channels(a.C) == 8) HTTM_NORM_BWD(1024, 8);
+  else switch (grad_threads(a.C)) {
+    case 32: HTTM_NORM_BWD(32, 4); break;
+    case 64: HTTM_NORM_BWD(64, 4); break;
+    case 128: HTTM_NORM_BWD(128, 4); break;
+    case 256: HTTM_NORM_BWD(256, 4); break;
+    case 512: HTTM_NORM_BWD(512, 4); break;
+    default: HTTM_NORM_BWD(1024, 4); break;
   }
 #undef HTTM_NORM_BWD
   return cudaGetLastError();
@@ -597,7 +690,8 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c->rows == 0 && !n_out) return HTTM_OK;
   HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto vec) {
-    return launch_grad<decltype(tx), decltype(tf), decltype(vec)::value>(a, s);
+    return post ? launch_grad<decltype(tx), decltype(tf), decltype(vec)::value, true>(a, s)
+                : launch_grad<decltype(tx), decltype(tf), decltype(vec)::value, false>(a, s);
   }), s);
   if (n_out) {
     sum.partial = a.partial;
@@ -605,8 +699,8 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
     sum.C = c->channels;
     sum.gates = a.gates;
     sum.chunks = a.chunks;
-    const dim3 grid((c->channels + 31) / 32, n_out, sum.is_gate0 ? a.gates : 1);
-    norm_sum_kernel<<<grid, dim3(32, 32), 0, s>>>(sum);
+    const dim3 grid((c->channels + 15) / 16, n_out, sum.is_gate0 ? a.gates : 1);
+    norm_sum_kernel<<<grid, dim3(16, 64), 0, s>>>(sum);
     HTTM_OPS_LAUNCH(cudaGetLastError(), s);
   }
   return HTTM_OK;
