@@ -88,6 +88,15 @@ CASES = [
     (1, 2, 2, 700, 300, 64, "none"),           # more queries than keys
     (1, 1, 1, 1500, 1500, 64, "none"),         # queries of a key tile split
     (1, 2, 1, 513, 130, 64, "random"),
+    # few rows a key head: one, 16, 17, 32 and (past them) 33
+    (1, 1, 1, 1, 31, 64, "none"),
+    (3, 16, 1, 1, 700, 64, "padded"),
+    (2, 17, 1, 1, 700, 32, "random"),
+    (2, 16, 1, 2, 9000, 64, "causal"),
+    (2, 11, 1, 3, 400, 64, "random"),
+    (5, 8, 2, 4, 333, 56, "window"),
+    (1, 1, 1, 32, 32, 64, "packed"),
+    (40, 8, 8, 1, 260, 64, "padded"),
 ]
 
 
@@ -183,6 +192,23 @@ def test_unseen_places_may_hold_anything():
     grads = ops.httm_attention_backward(dout, q, k, v, out, lse, b, e)
     for name, t in zip(("dq", "dk", "dv"), grads):
         assert torch.equal(t, want[name]), name
+
+
+def test_unseen_places_may_hold_anything_for_single_tokens():
+    """A cache whose entries behind each sequence's length were never
+    written, one sequence of length 0."""
+    B, H, K, N, d = 4, 8, 2, 500, 64
+    q, k, v, _ = _inputs(B, H, K, 1, N, d)
+    n = torch.tensor([500, 33, 0, 257], device="cuda")
+    b, e = ops.length_ranges(n, 1)
+    want = ops.httm_attention_forward(q, k, v, b, e)
+    unseen = (torch.arange(N, device="cuda")[None] >= n[:, None])[:, None, :, None]
+    q = q.clone()
+    q[2] = float("nan")
+    for bad in (float("nan"), float("inf")):
+        got = ops.httm_attention_forward(q, k.masked_fill(unseen, bad), v.masked_fill(unseen, bad), b, e)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (want[0][2] == 0).all() and (want[1][2] == -float("inf")).all()
 
 
 def test_visible_nan_reaches_its_row():

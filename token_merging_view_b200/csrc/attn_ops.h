@@ -35,12 +35,18 @@ struct AttnMap {
 bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch, int box);
 
 // Forward: work items of up to 256 query rows, each in `parts` key ranges.
+// With at most kAttnFewRows rows a key head the kernel for few rows runs.
+constexpr int kAttnFewRows = 32;
+constexpr int kAttnRangePart = 68;     // floats of a partial row: O (64), sum, maximum (log2), 2 unused
 struct AttnFwdPlan {
+  bool few;
   int rows, row_tiles, parts;           // rows = L * G of one key head
   long long items;                      // B * K * row_tiles
   size_t part_bytes;
 };
 AttnFwdPlan attn_fwd_plan(const httm_attention& a);
+int attn_rows_parts(const httm_attention& a);
+cudaError_t launch_attn_rows(const AttnArgs& a, const AttnFwdPlan& p, float* part_out, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s);
 
 // Backward workspace: per query row -lse * log2(e) and -D (D = dout . out),

@@ -41,7 +41,7 @@ using namespace tc;
 constexpr int kStages = 4;
 constexpr int kThreads = 384;
 constexpr uint32_t kColO = 384;           // O_t at kColO + 64 t; S ring at 0, 128, 256
-constexpr int kPartStride = 68;           // floats of a partial row: O (64), sum, max in use, 2 unused
+constexpr int kPartStride = httm::kAttnRangePart;
 
 struct FwdSmem {
   uint8_t q[2][kTileBytes];
@@ -432,6 +432,7 @@ AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
   p.rows = a.q_len * G;
   p.row_tiles = (p.rows + 255) / 256;
   p.items = (long long)a.batch * a.kv_heads * p.row_tiles;
+  p.few = p.rows <= kAttnFewRows;
   const long long tiles = (a.kv_len + kAttnTile - 1) / kAttnTile;
   p.parts = 1;
   double best = 0;
@@ -442,11 +443,26 @@ AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
     const double cost = (double)waves * ((tiles + n - 1) / n + 3) + (n > 1 ? 4 + n / 16.0 : 0);
     if (n == 1 || cost < best) best = cost, p.parts = n;
   }
+  if (p.few) p.parts = attn_rows_parts(a);
   p.part_bytes = p.parts > 1 ? (size_t)p.items * p.parts * std::min(p.rows, 256) * kPartStride * 4 : 0;
   return p;
 }
 
+namespace {
+cudaError_t launch_join(const AttnArgs& a, const AttnFwdPlan& p, const float* part, cudaStream_t s) {
+  if (p.parts == 1) return cudaSuccess;
+  const long long rows = (long long)a.B * a.K * p.rows;
+  attn_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a, p.row_tiles, p.parts, part);
+  return cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s) {
+  float* part = static_cast<float*>(ws);
+  if (p.few) {
+    const cudaError_t e = launch_attn_rows(a, p, part, s);
+    return e != cudaSuccess ? e : launch_join(a, p, part, s);
+  }
   AttnMap mk, mv;
   // without keys nothing is loaded through their maps
   if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B, kAttnTile) ||
@@ -456,11 +472,9 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, c
       cudaFuncSetAttribute(attn_range_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   attn_range_fwd_kernel<<<(unsigned)(p.items * p.parts), kThreads, kSmemBytes, s>>>(mk, mv, a, p.row_tiles, p.parts,
-                                                                                    static_cast<float*>(ws));
-  if ((e = cudaGetLastError()) != cudaSuccess || p.parts == 1) return e;
-  const long long rows = (long long)a.B * a.K * p.rows;
-  attn_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a, p.row_tiles, p.parts, static_cast<float*>(ws));
-  return cudaGetLastError();
+                                                                                    part);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_join(a, p, part, s);
 }
 
 }  // namespace httm
