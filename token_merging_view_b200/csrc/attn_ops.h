@@ -37,6 +37,7 @@ bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, i
 // Forward: work items of up to 256 query rows, each in `parts` key ranges.
 // With at most kAttnFewRows rows a key head the kernel for few rows runs.
 constexpr int kAttnFewRows = 32;
+constexpr int kAttnCluster = 8;         // parts of few rows that are added up inside one launch
 constexpr int kAttnRangePart = 68;     // floats of a partial row: O (64), sum, maximum (log2), 2 unused
 struct AttnFwdPlan {
   bool few;

@@ -444,7 +444,7 @@ AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
     if (n == 1 || cost < best) best = cost, p.parts = n;
   }
   if (p.few) p.parts = attn_rows_parts(a);
-  p.part_bytes = p.parts > 1 ? (size_t)p.items * p.parts * std::min(p.rows, 256) * kPartStride * 4 : 0;
+  p.part_bytes = p.parts > (p.few ? kAttnCluster : 1) ? (size_t)p.items * p.parts * std::min(p.rows, 256) * kPartStride * 4 : 0;
   return p;
 }
 
@@ -461,7 +461,7 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, c
   float* part = static_cast<float*>(ws);
   if (p.few) {
     const cudaError_t e = launch_attn_rows(a, p, part, s);
-    return e != cudaSuccess ? e : launch_join(a, p, part, s);
+    return e != cudaSuccess || p.parts <= kAttnCluster ? e : launch_join(a, p, part, s);
   }
   AttnMap mk, mv;
   // without keys nothing is loaded through their maps

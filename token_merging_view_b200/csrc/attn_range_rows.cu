@@ -10,7 +10,9 @@
 // with the 16-row warp-level MMAs (m16n8k16), and keeps a running maximum,
 // sum and O in registers.  Four warps a block and two blocks an SM keep about
 // 128 KB of loads in flight.  At the end the block's warps are added up in
-// order, then the blocks of an item (attn_join_kernel).
+// order, then the blocks of an item: up to 8 are a cluster and read each
+// other's shared memory (one launch, no workspace); more, for a long cache
+// with few items, go through the workspace and attn_join_kernel.
 #include <algorithm>
 
 #include "attn_ops.cuh"
@@ -25,10 +27,12 @@ constexpr int kKeys = 32;                             // keys of a warp's tile
 constexpr int kRing = 3;
 constexpr uint32_t kHalf = kKeys * kAttnD * 2;        // 4 KB: 32 rows x 64 bf16 (K or V)
 constexpr int kMaxRows = 32;
+constexpr int kCluster = kAttnCluster;                // parts of an item that form a cluster
 
 struct RowsSmem {
   uint8_t kv[kWarps][kRing][2][kHalf];                // reused for the warps' O at the end
   float m[kWarps][kMaxRows], l[kWarps][kMaxRows];
+  float bm[kMaxRows], bl[kMaxRows];                   // the block's
   uint64_t full[kWarps][kRing];
   int abort;
 };
@@ -54,8 +58,44 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// MT tiles of 16 rows.
-template <int MT>
+// The address of a shared-memory location in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Four channels of a finished row: O / l, and the log-sum-exp.
+__device__ __forceinline__ void put_row(const AttnArgs& a, int b, int kh, int r, int c, float4 v, float mx, float l) {
+  const int li = r / a.G, head = kh * a.G + (r - li * a.G);
+  const int2 kr = key_range(a, b, li);
+  const bool seen = kr.x < kr.y;
+  const float inv = seen ? 1.f / l : 0.f;
+  if (!seen) v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < a.d) {
+    __nv_bfloat16* dst =
+        reinterpret_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + head * a.out.sh + (int64_t)li * a.out.st;
+    *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  }
+  if (c == 0 && a.lse)
+    a.lse[((size_t)b * a.H + head) * a.L + li] = seen ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// MT tiles of 16 rows.  CLUSTER: the parts of an item are one cluster.
+template <int MT, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
                  const __grid_constant__ AttnArgs a, int parts, float* __restrict__ part_out) {
@@ -214,9 +254,9 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
     if (lane == 0 && i + kRing < n) load(i + kRing);
   }
   if (!__syncthreads_and(ok)) {
-    // a wait ran out: copies in flight land before the shared memory goes away
+    // a wait ran out: copies in flight land before the shared memory goes
+    // away; the outputs are undefined, but every block meets the barriers
     for (int i = 0; i < 200; ++i) __nanosleep(1000);
-    return;
   }
 
   // the warps' results, then their sum in order
@@ -253,7 +293,15 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
       l = fmaf(sm.l[w][r], f, l);
       v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
     }
-    if (parts > 1) {
+    if (CLUSTER) {
+      // over the first warp's O, which this thread alone reads here
+      float* own = reinterpret_cast<float*>(&sm.kv[0][0][0][0]);
+      *reinterpret_cast<float4*>(own + r * kAttnD + c) = v;
+      if (c == 0) {
+        sm.bm[r] = mx;
+        sm.bl[r] = l;
+      }
+    } else if (parts > 1) {
       float* dst = part_out + ((size_t)blockIdx.x * R + r) * kAttnRangePart;
       *reinterpret_cast<float4*>(dst + c) = v;
       if (c == 0) {
@@ -261,19 +309,28 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
         dst[kAttnD + 1] = mx;
       }
     } else {
-      const int li = r / a.G, head = kh * a.G + (r - li * a.G);
-      const int2 kr = key_range(a, b, li);
-      const bool seen = kr.x < kr.y;
-      const float inv = seen ? 1.f / l : 0.f;
-      if (!seen) v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < a.d) {
-        __nv_bfloat16* dst =
-            reinterpret_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + head * a.out.sh + (int64_t)li * a.out.st;
-        *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-      }
-      if (c == 0 && a.lse)
-        a.lse[((size_t)b * a.H + head) * a.L + li] = seen ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      put_row(a, b, kh, r, c, v, mx, l);
     }
+  }
+  if (CLUSTER) {
+    cluster_sync();
+    // each block finishes its share of the rows, reading the others' in order
+    for (int x = threadIdx.x; x < R * (kAttnD / 4); x += kWarps * 32) {
+      const int r = x / (kAttnD / 4), c = (x % (kAttnD / 4)) * 4;
+      if ((unsigned)r % parts != part) continue;
+      float mx = -INFINITY, l = 0.f;
+      for (int p = 0; p < parts; ++p) mx = fmaxf(mx, ld_cluster(in_block(&sm.bm[r], p)));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < parts; ++p) {
+        const float f = ex2(ld_cluster(in_block(&sm.bm[r], p)) - ref);
+        const float4 y = ld_cluster4(in_block(all + r * kAttnD + c, p));
+        l = fmaf(ld_cluster(in_block(&sm.bl[r], p)), f, l);
+        v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+      }
+      put_row(a, b, kh, r, c, v, mx, l);
+    }
+    cluster_sync();                                   // nobody leaves while its memory is read
   }
 }
 
@@ -282,18 +339,23 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
 // Parts of an item's keys: blocks stream about 128 keys (four warps' tiles)
 // at a time, and cost about four such rounds of start and end; two are
 // resident on an SM.  Where ranges are given the entries' lengths may differ,
-// so the items are cut in enough parts to even out.
+// so the items are cut in enough parts to even out.  Up to kCluster parts
+// cost little to add up (rounded to a power of two: clusters of other sizes
+// leave SMs idle); beyond that the join is a launch of its own.
 int attn_rows_parts(const httm_attention& a) {
   const long long items = (long long)a.batch * a.kv_heads, rounds = (a.kv_len + kWarps * kKeys - 1) / (kWarps * kKeys);
   const int slots = 2 * kSMs;
-  const long long even = a.key_end || a.key_begin ? (4ll * slots + items - 1) / std::max(1ll, items) : 1;
-  const int most = (int)std::min<long long>(kAttnMaxParts, std::max<long long>(1, rounds / 4));
+  const bool ragged = a.key_end || a.key_begin;
+  const int most = (int)std::min<long long>(kAttnMaxParts, std::max<long long>(1, rounds));
   int parts = 1;
   double best = 0;
-  for (int n = (int)std::min<long long>(most, even); n <= most && items > 0; ++n) {
-    if (best > 0 && items * n > 16 * slots) break;
+  for (int n = 1; n <= most && items > 0; ++n) {
+    if (n <= kCluster && (n & (n - 1)) != 0) continue;
+    if (n > 1 && items * n > 16 * slots) break;
     const long long waves = (items * n + slots - 1) / slots;
-    const double cost = (double)waves * ((rounds + n - 1) / n + 4) + (n > 1 ? 3 + n / 8.0 : 0);
+    double cost = (double)waves * ((rounds + n - 1) / n + 4) + (n > kCluster ? 4 + n / 8.0 : n > 1 ? 1 : 0);
+    // ragged items: the longest part bounds the last wave
+    if (ragged && waves < 4) cost += (double)(rounds + n - 1) / n * (4 - waves) / 4;
     if (best == 0 || cost < best) best = cost, parts = n;
   }
   return parts;
@@ -304,11 +366,22 @@ cudaError_t launch_attn_rows(const AttnArgs& a, const AttnFwdPlan& p, float* par
   // without keys nothing is loaded through their maps
   if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B, kKeys) || !attn_map(&mv, a.v, a.q.data, a.d, a.N, a.K, a.B, kKeys))
     return cudaErrorInvalidValue;
-  auto kernel = p.rows <= 16 ? attn_rows_kernel<1> : attn_rows_kernel<2>;
+  const bool cluster = p.parts > 1 && p.parts <= kCluster;
+  auto kernel = p.rows <= 16 ? (cluster ? attn_rows_kernel<1, true> : attn_rows_kernel<1, false>)
+                             : (cluster ? attn_rows_kernel<2, true> : attn_rows_kernel<2, false>);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(p.items * p.parts), kWarps * 32, kRowsSmem, s>>>(mk, mv, a, p.parts, part_out);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.items * p.parts));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kRowsSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim = {(unsigned)p.parts, 1, 1};
+  cfg.attrs = &at;
+  cfg.numAttrs = cluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, a, p.parts, part_out);
 }
 
 }  // namespace httm

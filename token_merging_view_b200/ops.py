@@ -113,7 +113,7 @@ def _heads_shape(t, name):
 
 
 def _new_like(t):
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(*t.shape, dtype=t.dtype, device=t.device)
 
 
 def _same(t, like, name):
@@ -165,7 +165,7 @@ def _attention_bytes(cfg):
 def _lse(lse, q):
     shape = q.shape[:-1]
     if lse is None:
-        return torch.empty(shape, dtype=torch.float32, device=q.device)
+        return torch.empty(*shape, dtype=torch.float32, device=q.device)
     if lse.shape != shape or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 {list(shape)} tensor")
     return lse
@@ -385,7 +385,7 @@ def _norm_tensors(post, pre):
 
 def _stats(stats, rows, like):
     if stats is None:
-        return torch.empty((4, rows), dtype=torch.float32, device=like.device)
+        return torch.empty(4, rows, dtype=torch.float32, device=like.device)
     if stats.dtype != torch.float32 or stats.shape != (4, rows) or not stats.is_contiguous():
         raise ValueError(f"stats must be a contiguous float32 [4, {rows}] tensor")
     return stats
@@ -417,7 +417,7 @@ def httm_gated_norm_forward(x, f=None, gate=None, post=None, pre=None, residual_
             if z is not None:
                 raise ValueError("z without pre")
         elif z is None:
-            z = torch.empty(shape, dtype=bdt, device=x.device)
+            z = torch.empty(*shape, dtype=bdt, device=x.device)
         stats = _stats(stats, shape[0], x)
         st = load_library().httm_gated_norm_forward(
             cfg, weights, _rows(x, shape, "x", xdt), None if f is None else _rows(f, shape, "f", bdt),
