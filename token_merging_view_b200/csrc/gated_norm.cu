@@ -46,13 +46,23 @@ struct NormArgs {
 };
 enum { kGate = 0, kPostW, kPostB, kPreW, kPreB, kNumGrads };
 
-// E neighbouring elements, 4 or 8, as raw words: bf16 pairs or fp32.
-template <class T, int E>
+// W neighbouring elements, 1 to 8, as raw words: bf16 pairs (a single bf16 in
+// the low half) or fp32.  Converted when they are used, so a row in flight
+// costs few registers and nothing waits for it.
+template <class T, int W>
 struct Words {
-  static constexpr int n = E * (int)sizeof(T) / 4;
+  static constexpr int n = W * (int)sizeof(T) <= 4 ? 1 : W * (int)sizeof(T) / 4;
   uint32_t w[n];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < n; ++i) w[i] = 0u;
+  }
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (n == 2) {
+    if constexpr (W * sizeof(T) == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (n == 1) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (n == 2) {
       const uint2 x = *reinterpret_cast<const uint2*>(p);
       w[0] = x.x, w[1] = x.y;
     } else {
@@ -63,27 +73,28 @@ struct Words {
       }
     }
   }
-  __device__ __forceinline__ void get(float (&v)[E]) const {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if constexpr (sizeof(T) == 4) v[e] = __uint_as_float(w[e]);
-      else v[e] = __uint_as_float((e & 1) ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-    }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    return __uint_as_float((e & 1) ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
   }
-  __device__ __forceinline__ void set(const float (&v)[E]) {
+  __device__ __forceinline__ void set(const float* v) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = __float_as_uint(v[e]);
+      for (int e = 0; e < W; ++e) w[e] = __float_as_uint(v[e]);
     } else {
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+      for (int e = 0; e < n; ++e) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], W == 1 ? 0.f : v[2 * e + 1]);
         w[e] = *reinterpret_cast<const uint32_t*>(&b);
       }
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (n == 2) {
+    if constexpr (W * sizeof(T) == 2) {
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+    } else if constexpr (n == 1) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (n == 2) {
       *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
@@ -93,69 +104,57 @@ struct Words {
   }
 };
 
-// The channels of a thread.  VEC: vector v covers E neighbouring channels,
-// in one or two wide accesses (channels a multiple of 8, rows aligned); else
-// the E are NT apart, so that neighbouring threads touch neighbouring
-// elements.
-template <int NT, bool VEC, int E = 8>
+// The channels of a thread: E of them at v, as E / W vectors of W neighbours.
+// W is E where the channels are a multiple of 8 and every row starts on 16
+// bytes, 2 where rows allow pairs, else 1; the vectors of a thread are NT
+// apart, so that neighbouring threads touch neighbouring memory.
+template <int NT, int W, int E = 8>
 struct Cols {
   int t, C;
-  __device__ __forceinline__ int at(int v, int e) const { return VEC ? (v * NT + t) * E + e : (v * E + e) * NT + t; }
-  __device__ __forceinline__ bool live(int v, int e) const { return at(v, VEC ? 0 : e) < C; }
+  __device__ __forceinline__ int at(int v, int e) const { return ((v * (E / W) + e / W) * NT + t) * W + e % W; }
+  __device__ __forceinline__ bool live(int v, int e) const { return at(v, e / W * W) < C; }
   // elements behind the row's end read as 0
   template <class T>
   __device__ __forceinline__ void load(const T* row, int v, float (&r)[E]) const {
-    if constexpr (VEC) {
-      if (live(v, 0)) {
-        Words<T, E> w;
-        w.load(row + at(v, 0));
-        w.get(r);
-      } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) r[e] = 0.f;
-      }
-    } else {
+    for (int e = 0; e < E; e += W) {
+      Words<T, W> w;
+      w.clear();
+      if (live(v, e)) w.load(row + at(v, e));
 #pragma unroll
-      for (int e = 0; e < E; ++e) r[e] = live(v, e) ? to_f(row[at(v, e)]) : 0.f;
+      for (int i = 0; i < W; ++i) r[e + i] = w.get(i);
     }
   }
   template <class T>
   __device__ __forceinline__ void store(T* row, int v, const float (&r)[E]) const {
-    if constexpr (VEC) {
-      if (live(v, 0)) {
-        Words<T, E> w;
-        w.set(r);
-        w.store(row + at(v, 0));
-      }
-    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (live(v, e)) row[at(v, e)] = from_f<T>(r[e]);
-    }
+    for (int e = 0; e < E; e += W)
+      if (live(v, e)) {
+        Words<T, W> w;
+        w.set(r + e);
+        w.store(row + at(v, e));
+      }
   }
 };
 
-// A row's E channels of a thread as loaded, converted when they are used: a
-// row in flight costs few registers.
-template <class T, int NT, bool VEC, int E>
+// A row's E channels of a thread as loaded.
+template <class T, int NT, int W, int E>
 struct Raw {
-  using W = std::conditional_t<VEC, Words<T, E>, Words<float, E>>;
-  W words;
+  Words<T, W> words[E / W];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < W::n; ++i) words.w[i] = 0u;
+    for (int i = 0; i < E / W; ++i) words[i].clear();
   }
-  __device__ __forceinline__ void load(const Cols<NT, VEC, E>& cols, const void* base, int64_t row, int64_t stride) {
+  __device__ __forceinline__ void load(const Cols<NT, W, E>& cols, const void* base, int64_t row, int64_t stride) {
     const T* p = static_cast<const T*>(base) + row * stride;
-    if constexpr (VEC) {
-      if (cols.live(0, 0)) words.load(p + cols.at(0, 0));
-    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (cols.live(0, e)) words.w[e] = __float_as_uint(to_f(p[cols.at(0, e)]));
-    }
+    for (int e = 0; e < E; e += W)
+      if (cols.live(0, e)) words[e / W].load(p + cols.at(0, e));
   }
-  __device__ __forceinline__ void get(float (&v)[E]) const { words.get(v); }
+  __device__ __forceinline__ void get(float (&v)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = words[e / W].get(e % W);
+  }
 };
 
 // Sum over the NT threads of a row (all of them get it).  NT = 32: shuffles;
@@ -179,8 +178,8 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*tmp)[K][32], int
 }
 
 // n = (v - mean) * r in place; returns mean and r.
-template <int NT, bool VEC, int V>
-__device__ __forceinline__ void normalise(float (&v)[V][8], const Cols<NT, VEC>& cols, int kind, float eps, float inv_c,
+template <int NT, int W, int V>
+__device__ __forceinline__ void normalise(float (&v)[V][8], const Cols<NT, W>& cols, int kind, float eps, float inv_c,
                                           float (*tmp)[1][32], int& turn, float& mean, float& r) {
   mean = 0.f;
   float s[1];
@@ -209,8 +208,8 @@ __device__ __forceinline__ void normalise(float (&v)[V][8], const Cols<NT, VEC>&
     for (int e = 0; e < 8; ++e) v[i][e] *= r;
 }
 
-template <int NT, bool VEC, int V>
-__device__ __forceinline__ void affine(float (&v)[V][8], const Cols<NT, VEC>& cols, const float* w, const float* b) {
+template <int NT, int W, int V>
+__device__ __forceinline__ void affine(float (&v)[V][8], const Cols<NT, W>& cols, const float* w, const float* b) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float g[8], o[8];
@@ -227,14 +226,14 @@ __device__ __forceinline__ void affine(float (&v)[V][8], const Cols<NT, VEC>& co
   }
 }
 
-template <class TX, class TF, int NT, int V, bool VEC>
+template <class TX, class TF, int NT, int V, int W>
 __global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs a) {
   constexpr int kRows = NT > 32 ? 1 : 4;                      // rows per block (barriers need one)
   __shared__ float tmp[2][1][32];
   int turn = 0;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
   if (row >= a.rows) return;                                  // whole warps: NT is a multiple of 32
-  const Cols<NT, VEC> cols{(int)(threadIdx.x % NT), a.C};
+  const Cols<NT, W> cols{(int)(threadIdx.x % NT), a.C};
   const float inv_c = 1.f / (float)a.C;
   float f[V][8], y[V][8];
 #pragma unroll
@@ -245,12 +244,12 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs
   }
   if (a.post != HTTM_NORM_NONE) {
     float mean, r;
-    normalise<NT, VEC, V>(f, cols, a.post, a.post_eps, inv_c, tmp, turn, mean, r);
+    normalise<NT, W, V>(f, cols, a.post, a.post_eps, inv_c, tmp, turn, mean, r);
     if (a.stats && cols.t == 0) {
       a.stats[row] = mean;
       a.stats[a.rows + row] = r;
     }
-    affine<NT, VEC, V>(f, cols, a.post_w, a.post_b);
+    affine<NT, W, V>(f, cols, a.post_w, a.post_b);
   }
   if (a.gate) {
     const float* g = a.gate + (row / a.gate_rows) * a.C;
@@ -275,12 +274,12 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs
   }
   if (a.pre != HTTM_NORM_NONE) {
     float mean, r;
-    normalise<NT, VEC, V>(y, cols, a.pre, a.pre_eps, inv_c, tmp, turn, mean, r);
+    normalise<NT, W, V>(y, cols, a.pre, a.pre_eps, inv_c, tmp, turn, mean, r);
     if (a.stats && cols.t == 0) {
       a.stats[2 * a.rows + row] = mean;
       a.stats[3 * a.rows + row] = r;
     }
-    affine<NT, VEC, V>(y, cols, a.pre_w, a.pre_b);
+    affine<NT, W, V>(y, cols, a.pre_w, a.pre_b);
 #pragma unroll
     for (int i = 0; i < V; ++i) cols.store(static_cast<TF*>(a.z) + row * a.sz, i, y[i]);
   }
@@ -301,7 +300,7 @@ constexpr int grad_blocks(int NT, int E) { return E == 8 || NT == 1024 ? 1 : 768
 // group's rows with E channels a thread, one row ahead with its loads.  POST:
 // there is a norm on the block's output (two more parameter gradients and
 // another pair of sums a row).
-template <class TX, class TF, int NT, bool VEC, bool POST, int E>
+template <class TX, class TF, int NT, int W, bool POST, int E>
 __global__ void __launch_bounds__(NT > 32 ? NT : 128, grad_blocks(NT, E))
 gated_norm_grad_kernel(NormArgs a) {
   constexpr int kGroups = NT > 32 ? 1 : 4;                    // thread groups per block (barriers need one)
@@ -310,7 +309,7 @@ gated_norm_grad_kernel(NormArgs a) {
   const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / NT;
   const int n_gates = max(1, a.gates);
   if (group >= (int64_t)n_gates * a.chunks) return;
-  const Cols<NT, VEC, E> cols{(int)(threadIdx.x % NT), a.C};
+  const Cols<NT, W, E> cols{(int)(threadIdx.x % NT), a.C};
   const float inv_c = 1.f / (float)a.C;
   const int gq = (int)(group / a.chunks), chunk = (int)(group % a.chunks);
   const int64_t r0 = gq * a.gate_rows + a.gate_rows * chunk / a.chunks;
@@ -336,8 +335,8 @@ gated_norm_grad_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
 
-  Raw<TX, NT, VEC, E> next_dy, next_y;
-  Raw<TF, NT, VEC, E> next_f, next_dz;
+  Raw<TX, NT, W, E> next_dy, next_y;
+  Raw<TF, NT, W, E> next_f, next_dz;
   next_dy.clear();
   next_y.clear();
   next_f.clear();
@@ -438,7 +437,7 @@ struct SumArgs {
 };
 
 // Adds up the partial rows: 16 channels a block, 64 threads down the rows,
-// each in order, then the 64 in order.
+// each in order, then the 64 in a fixed tree.
 __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
   __shared__ float s[64][17];
   const int k = blockIdx.y, col = blockIdx.x * 16 + threadIdx.x;
@@ -449,17 +448,21 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
   float v = 0.f;
   if (col < a.C) {
     const float* p = a.partial + ((int64_t)k * n_part + p0) * a.C + col;
-#pragma unroll 8
-    for (int64_t i = threadIdx.y; i < n; i += 64) v += p[i * a.C];
+    for (int64_t i = threadIdx.y; i < n; i += 64 * 8) {       // 8 loads in flight
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = i + u * 64 < n ? p[(i + u * 64) * a.C] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += x[u];
+    }
   }
   s[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y == 0 && col < a.C) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) t += s[i][threadIdx.x];
-    a.out[k][(per_gate ? (int64_t)blockIdx.z * a.C : 0) + col] = t;
+  for (int h = 32; h > 0; h >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.y < h) s[threadIdx.y][threadIdx.x] += s[threadIdx.y + h][threadIdx.x];
   }
+  if (threadIdx.y == 0 && col < a.C)
+    a.out[k][(per_gate ? (int64_t)blockIdx.z * a.C : 0) + col] = s[0][threadIdx.x];
 }
 
 // Thread groups per gate group of the backward kernel: as many as the SMs
@@ -472,13 +475,13 @@ int grad_chunks(const httm_norm_cfg& c) {
   return (int)std::max<int64_t>(1, std::min(want, rows / 4));
 }
 
-template <class TX, class TF, bool VEC>
+template <class TX, class TF, int W>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
 #define HTTM_NORM_FWD(NT, V)                                                                        \
   do {                                                                                              \
     constexpr int kRows = (NT) > 32 ? 1 : 4;                                                        \
     const int64_t grid = (a.rows + kRows - 1) / kRows;                                              \
-    gated_norm_kernel<TX, TF, NT, V, VEC><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a);     \
+    gated_norm_kernel<TX, TF, NT, V, W><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a);     \
   } while (0)
   if (a.C <= 256) HTTM_NORM_FWD(32, 1);
   else if (a.C <= 512) HTTM_NORM_FWD(32, 2);
@@ -490,13 +493,13 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <class TX, class TF, bool VEC, bool POST>
+template <class TX, class TF, int W, bool POST>
 cudaError_t launch_grad(const NormArgs& a, cudaStream_t s) {
 #define HTTM_NORM_BWD(NT, E)                                                                          \
   do {                                                                                                \
     constexpr int kGroups = (NT) > 32 ? 1 : 4;                                                        \
     const int64_t grid = ((int64_t)std::max(1, a.gates) * a.chunks + kGroups - 1) / kGroups;          \
-    gated_norm_grad_kernel<TX, TF, NT, VEC, POST, E><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a); \
+    gated_norm_grad_kernel<TX, TF, NT, (W < E ? W : E), POST, E><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a); \
   } while (0)
   if (grad_channels(a.C) == 8) HTTM_NORM_BWD(1024, 8);
   else switch (grad_threads(a.C)) {
@@ -529,29 +532,38 @@ httm_status check_cfg(const httm_norm_cfg* c) {
 size_t elem(int dtype) { return dtype == HTTM_F32 ? 4 : 2; }
 
 // A [rows, C] argument: present, aligned to its type, and (an output) with
-// rows that do not overlap.  Clears *wide when it needs element accesses.
-httm_status check_rows(const httm_rows* r, int64_t rows, int C, int dtype, bool output, bool* wide) {
+// rows that do not overlap.  Narrows *width to the elements (8, 2 or 1) that
+// all accesses can take at a time.
+httm_status check_rows(const httm_rows* r, int64_t rows, int C, int dtype, bool output, int* width) {
   if (!r->data) return HTTM_ERR_ARG;
   if (!aligned(r->data, elem(dtype))) return HTTM_ERR_ALIGN;
   if (output && rows > 1 && (r->row < 0 ? -r->row : r->row) < C) return HTTM_ERR_ARG;
-  if (!aligned(r->data, 16) || (rows > 1 && r->row % (int64_t)(16 / elem(dtype)) != 0)) *wide = false;
+  const int64_t row = rows > 1 ? r->row : 0;
+  if (!aligned(r->data, 16) || row % (int64_t)(16 / elem(dtype)) != 0) *width = std::min(*width, 2);
+  if (!aligned(r->data, 2 * elem(dtype)) || row % 2 != 0) *width = 1;
   return HTTM_OK;
 }
-httm_status check_param(const float* p, bool* wide) {
+httm_status check_param(const float* p, int* width) {
   if (!p) return HTTM_OK;
   if (!aligned(p, 4)) return HTTM_ERR_ALIGN;
-  if (!aligned(p, 16)) *wide = false;
+  if (!aligned(p, 16)) *width = std::min(*width, 2);
+  if (!aligned(p, 8)) *width = 1;
   return HTTM_OK;
 }
+int row_width(int C) { return C % 8 == 0 ? 8 : C % 2 == 0 ? 2 : 1; }
 
+template <class TX, class TF, class Fn>
+cudaError_t by_width(int width, Fn&& fn) {
+  if (width == 8) return fn(TX{}, TF{}, std::integral_constant<int, 8>{});
+  if (width == 2) return fn(TX{}, TF{}, std::integral_constant<int, 2>{});
+  return fn(TX{}, TF{}, std::integral_constant<int, 1>{});
+}
 template <class Fn>
-cudaError_t by_type(const httm_norm_cfg& c, bool wide, Fn&& fn) {
+cudaError_t by_type(const httm_norm_cfg& c, int width, Fn&& fn) {
   using bf16 = __nv_bfloat16;
-  if (c.stream_dtype == HTTM_F32 && c.branch_dtype == HTTM_F32)
-    return wide ? fn(float{}, float{}, std::true_type{}) : fn(float{}, float{}, std::false_type{});
-  if (c.stream_dtype == HTTM_F32)
-    return wide ? fn(float{}, bf16{}, std::true_type{}) : fn(float{}, bf16{}, std::false_type{});
-  return wide ? fn(bf16{}, bf16{}, std::true_type{}) : fn(bf16{}, bf16{}, std::false_type{});
+  if (c.branch_dtype == HTTM_F32) return by_width<float, float>(width, fn);
+  if (c.stream_dtype == HTTM_F32) return by_width<float, bf16>(width, fn);
+  return by_width<bf16, bf16>(width, fn);
 }
 
 }  // namespace
@@ -576,7 +588,7 @@ httm_status httm_gated_norm_forward(const httm_norm_cfg* c, const httm_norm_weig
   if (!f && (c->post != HTTM_NORM_NONE || c->gates > 0)) return HTTM_ERR_ARG;
   if (!y && (f || c->residual_scale != 1.f || !z)) return HTTM_ERR_ARG;
   if (c->rows == 0) return HTTM_OK;
-  bool wide = c->channels % 8 == 0;
+  int wide = row_width(c->channels);   // elements an access takes
   NormArgs a{};
   HTTM_TRY(check_rows(x, c->rows, c->channels, c->stream_dtype, false, &wide));
   a.x = x->data, a.sx = x->row;
@@ -605,8 +617,8 @@ httm_status httm_gated_norm_forward(const httm_norm_cfg* c, const httm_norm_weig
   a.post = c->post, a.pre = c->pre;
   a.post_eps = c->post_eps, a.pre_eps = c->pre_eps, a.rs = c->residual_scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto vec) {
-    return launch_forward<decltype(tx), decltype(tf), decltype(vec)::value>(a, s);
+  HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto width) {
+    return launch_forward<decltype(tx), decltype(tf), decltype(width)::value>(a, s);
   }), s);
   return HTTM_OK;
 }
@@ -632,7 +644,7 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
   if ((grads->gate && !c->gates) || ((grads->post_weight || grads->post_bias) && !post) ||
       ((grads->pre_weight || grads->pre_bias) && !pre))
     return HTTM_ERR_ARG;
-  bool wide = c->channels % 8 == 0;
+  int wide = row_width(c->channels);   // elements an access takes
   NormArgs a{};
   if (c->rows > 0) {
     if (dy) {
@@ -662,7 +674,7 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
   }
   for (const float* p : {w->gate, w->post_weight, w->post_bias, w->pre_weight, w->pre_bias})
     HTTM_TRY(check_param(p, &wide));
-  bool any = true;
+  int any = 8;
   for (const float* p : {grads->gate, grads->post_weight, grads->post_bias, grads->pre_weight, grads->pre_bias})
     HTTM_TRY(check_param(p, &any));
   if (stats && !aligned(stats, 4)) return HTTM_ERR_ALIGN;
@@ -690,9 +702,9 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
   a.rs = c->residual_scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c->rows == 0 && !n_out) return HTTM_OK;
-  HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto vec) {
-    return post ? launch_grad<decltype(tx), decltype(tf), decltype(vec)::value, true>(a, s)
-                : launch_grad<decltype(tx), decltype(tf), decltype(vec)::value, false>(a, s);
+  HTTM_OPS_LAUNCH(by_type(*c, wide, [&](auto tx, auto tf, auto width) {
+    return post ? launch_grad<decltype(tx), decltype(tf), decltype(width)::value, true>(a, s)
+                : launch_grad<decltype(tx), decltype(tf), decltype(width)::value, false>(a, s);
   }), s);
   if (n_out) {
     sum.partial = a.partial;

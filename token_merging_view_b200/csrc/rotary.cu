@@ -36,28 +36,30 @@ struct RotaryArgs {
   int inverse;
 };
 
-// W consecutive elements as floats; W = 8 goes in 16-byte accesses.
+// W consecutive elements as they lie in memory; W = 8 goes in 16-byte accesses.
 template <class T, int W>
-__device__ __forceinline__ void load_w(const T* p, float (&v)[W]) {
-  if constexpr (W == 1) {
-    v[0] = to_f(*p);
-  } else if constexpr (sizeof(T) == 4) {
+struct Vec {
+  static constexpr int n = W == 1 ? 1 : W * (int)sizeof(T) / 4;
+  uint32_t w[n];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (W == 1) {
+      w[0] = __float_as_uint(to_f(*p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const float4 x = reinterpret_cast<const float4*>(p)[i];
-      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-    }
-  } else {
-    static_assert(W == 8, "bf16 vectors are 16 bytes");
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      for (int i = 0; i < n / 4; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
     }
   }
-}
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      if constexpr (W == 1 || sizeof(T) == 4) v[e] = __uint_as_float(w[e]);
+      else v[e] = __uint_as_float((e & 1) ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+  }
+};
 template <class T, int W>
 __device__ __forceinline__ void store_w(T* p, const float (&v)[W]) {
   if constexpr (W == 1) {
@@ -97,6 +99,11 @@ __device__ __forceinline__ void turn_pair(float a, float b, float c, float s, fl
   x = fmaf(a, c, -__fmul_rn(b, s));
   y = fmaf(b, c, __fmul_rn(a, s));
 }
+
+// heads read ahead: 185 us without, 139 with 4, 130 with 8 (41,070 tokens x 32
+// heads, twice); the element accesses of odd shapes are slower with 8
+template <int W>
+constexpr int kHeadsAhead = W == 8 ? 8 : 4;
 
 template <class T, int W, bool HALF>
 __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a) {
@@ -141,33 +148,49 @@ __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a) {
     }
   }
 
+  // several heads are read before the first of them is written (in place, a
+  // thread writes only what it has read)
   const int h0 = hg * a.heads_per, h1 = min(h0 + a.heads_per, a.heads[0] + a.heads[1]);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const int which = h >= a.heads[0] ? 1 : 0, hh = which ? h - a.heads[0] : h;
-    const View &vi = a.in[which], &vo = a.out[which];
-    const T* x = reinterpret_cast<const T*>(vi.data) + b * vi.sb + hh * vi.sh + tok * vi.st;
-    T* y = reinterpret_cast<T*>(vo.data) + b * vo.sb + hh * vo.sh + tok * vo.st;
-    float u[W], v[W];
-    load_w<T, W>(x + lo, u);
-    if (copied) {
-      store_w<T, W>(y + lo, u);
-      continue;
-    }
-    load_w<T, W>(x + hi, v);
-    float p[W], q[W];
-    if constexpr (HALF || W == 1) {
+  auto row = [&](const View (&v)[2], int h) {
+    const int which = h >= a.heads[0] ? 1 : 0;
+    return reinterpret_cast<T*>(v[which].data) + b * v[which].sb + (h - (which ? a.heads[0] : 0)) * v[which].sh +
+           tok * v[which].st;
+  };
+  constexpr int kBatch = kHeadsAhead<W>;
+  for (int h = h0; h < h1; h += kBatch) {
+    Vec<T, W> x[kBatch], y[kBatch];
 #pragma unroll
-      for (int e = 0; e < W; ++e) turn_pair(u[e], v[e], c[e], s[e], p[e], q[e]);
-    } else {                               // pairs lie side by side in the 2 W channels (u, v)
-#pragma unroll
-      for (int e = 0; e < W / 2; ++e) {
-        turn_pair(u[2 * e], u[2 * e + 1], c[e], s[e], p[2 * e], p[2 * e + 1]);
-        turn_pair(v[2 * e], v[2 * e + 1], c[e + W / 2], s[e + W / 2], q[2 * e], q[2 * e + 1]);
+    for (int i = 0; i < kBatch; ++i)
+      if (h + i < h1) {
+        const T* src = row(a.in, h + i);
+        x[i].load(src + lo);
+        if (!copied) y[i].load(src + hi);
       }
-    }
-    store_w<T, W>(y + lo, p);
-    store_w<T, W>(y + hi, q);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (h + i < h1) {
+        T* dst = row(a.out, h + i);
+        float u[W], v[W];
+        x[i].get(u);
+        if (copied) {
+          store_w<T, W>(dst + lo, u);
+          continue;
+        }
+        y[i].get(v);
+        float p[W], q[W];
+        if constexpr (HALF || W == 1) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) turn_pair(u[e], v[e], c[e], s[e], p[e], q[e]);
+        } else {                           // pairs lie side by side in the 2 W channels (u, v)
+#pragma unroll
+          for (int e = 0; e < W / 2; ++e) {
+            turn_pair(u[2 * e], u[2 * e + 1], c[e], s[e], p[2 * e], p[2 * e + 1]);
+            turn_pair(v[2 * e], v[2 * e + 1], c[e + W / 2], s[e + W / 2], q[2 * e], q[2 * e + 1]);
+          }
+        }
+        store_w<T, W>(dst + lo, p);
+        store_w<T, W>(dst + hi, q);
+      }
   }
 }
 

@@ -332,7 +332,7 @@ def httm_rotary(q, k, freqs, positions, axes=1, layout=HTTM_ROTARY_HALF, factor=
 
 
 # ------------------------------------------------------------------ gated norm
-@dataclass(frozen=True)
+@dataclass(slots=True)
 class Norm:
     """A LayerNorm or RMSNorm: kind, float32 weight and bias (None: 1 / 0)."""
     kind: int
