@@ -440,11 +440,12 @@ struct SumArgs {
 // each in order, then the 64 in a fixed tree.
 __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
   __shared__ float s[64][17];
-  const int k = blockIdx.y, col = blockIdx.x * 16 + threadIdx.x;
-  const bool per_gate = k == 0 && a.is_gate0;
+  // blockIdx.y: the gate rows first (if wanted), then the other gradients
+  const int y = blockIdx.y, col = blockIdx.x * 16 + threadIdx.x;
+  const bool per_gate = a.is_gate0 && y < a.gates;
+  const int k = per_gate ? 0 : a.is_gate0 ? y - a.gates + 1 : y, gate = per_gate ? y : 0;
   const int64_t n_part = (int64_t)a.gates * a.chunks;
-  const int64_t p0 = per_gate ? (int64_t)blockIdx.z * a.chunks : 0, n = per_gate ? a.chunks : n_part;
-  if (!per_gate && blockIdx.z > 0) return;
+  const int64_t p0 = (int64_t)gate * a.chunks, n = per_gate ? a.chunks : n_part;
   float v = 0.f;
   if (col < a.C) {
     const float* p = a.partial + ((int64_t)k * n_part + p0) * a.C + col;
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
     if ((int)threadIdx.y < h) s[threadIdx.y][threadIdx.x] += s[threadIdx.y + h][threadIdx.x];
   }
   if (threadIdx.y == 0 && col < a.C)
-    a.out[k][(per_gate ? (int64_t)blockIdx.z * a.C : 0) + col] = s[0][threadIdx.x];
+    a.out[k][(int64_t)gate * a.C + col] = s[0][threadIdx.x];
 }
 
 // Thread groups per gate group of the backward kernel: as many as the SMs
@@ -712,7 +713,7 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
     sum.C = c->channels;
     sum.gates = a.gates;
     sum.chunks = a.chunks;
-    const dim3 grid((c->channels + 15) / 16, n_out, sum.is_gate0 ? a.gates : 1);
+    const dim3 grid((c->channels + 15) / 16, n_out + (sum.is_gate0 ? a.gates - 1 : 0));
     norm_sum_kernel<<<grid, dim3(16, 64), 0, s>>>(sum);
     HTTM_OPS_LAUNCH(cudaGetLastError(), s);
   }
