@@ -455,19 +455,13 @@ def httm_gated_norm_backward(dy, dz, f, y, stats, gate=None, post=None, pre=None
                 raise ValueError("df without f")
         elif df is None:
             df = _new_like(f)
-        # all parameter gradients in one allocation
-        sizes = [0 if t is None else t.numel() for t in params]
-        flat = torch.empty(sum(sizes), dtype=torch.float32, device=y.device) if any(sizes) else None
-        grads, at = [], 0
-        for t, n in zip(params, sizes):
-            grads.append(None if t is None else flat[at:at + n] if t.dim() == 1 else flat[at:at + n].view(t.shape))
-            at += n
+        grads = [None if t is None else torch.empty_like(t) for t in params]
         need = ctypes.c_size_t(0)
         lib = load_library()
         st = lib.httm_gated_norm_workspace_bytes(cfg, ctypes.addressof(need))
         if st:
             _check(st, "httm_gated_norm_workspace_bytes")
-        ws, n, keep = _workspace(workspace, need.value if flat is not None else 0, y)
+        ws, n, keep = _workspace(workspace, need.value if any(t is not None for t in grads) else 0, y)
         rows = [None if t is None else _rows(t, shape, name, dt) for name, t, dt in
                 (("dy", dy, sdt), ("dz", dz, bdt), ("f", f, bdt), ("y", y, sdt), ("dx", dx, sdt), ("df", df, bdt))]
         st = lib.httm_gated_norm_backward(cfg, weights, *rows[:4], stats.data_ptr(), *rows[4:],
