@@ -457,17 +457,17 @@ typedef struct {
  *  d_head            8 to 64 in steps of 8 (the tiles are 64 wide: a
  *                    narrower head costs as much as one of 64).
  *  dtype             HTTM_BF16 (other types: HTTM_ERR_UNSUPPORTED).
- *  softmax_scale     0 selects 1 / sqrt(d_head); negative or not finite:
- *                    HTTM_ERR_ARG.
+ *  softmax_scale     0 selects 1 / sqrt(d_head); else within 2^-64 .. 2^64
+ *                    (HTTM_ERR_ARG otherwise).
  *  key_begin, key_end  DEVICE int32 [batch, q_len], or NULL: 0 / kv_len.
  * A query whose range is empty has out = 0, lse = -infinity and takes no
- * part in the gradients.  What lies outside every range is not read into
- * any result: a key or value no query of its batch entry attends to, and a
+ * part in the gradients.  What lies outside the ranges is not read into any
+ * result: a key or value no query of its batch entry attends to, and a
  * query, dout or out row whose range is empty, may hold anything (infinities
- * and NaN too).  A non-finite value that some query does attend to may
- * reach every query within 256 rows of that one, also those that do not see
- * it, and so may a non-finite query or dout row in the gradients of the keys
- * of its tiles.
+ * and NaN too).  A non-finite key or value that some queries attend to
+ * reaches the outputs of those queries and no others.  In the gradients a
+ * non-finite q, k, v or dout row that takes part may also reach rows of its
+ * tiles (128 rows around it) that do not see it.
  * Strides are multiples of 8 elements and data pointers 16-byte aligned
  * (else HTTM_ERR_ALIGN).  Inputs may be broadcast (stride 0 over batch or
  * heads; their gradients are then those of every copy, for the caller to

@@ -222,6 +222,40 @@ def test_visible_nan_reaches_its_row():
     assert torch.isfinite(out[0, 0, rows]).all() and torch.isfinite(lse[0, 0, rows]).all()
 
 
+@pytest.mark.parametrize("G,L,N,mask", [(1, 300, 300, "causal"), (2, 300, 700, "random"), (1, 7, 90, "causal"),
+                                        (4, 6, 1000, "random"), (1, 600, 5000, "window"), (1, 9, 20000, "random")])
+def test_values_reach_only_the_rows_that_see_them(G, L, N, mask):
+    """Infinities and NaN in values (and NaN in keys) that some rows see and
+    some do not: the others keep their bits, and those that see an infinity in
+    a channel have it there."""
+    K, d = 2, 64
+    q, k, v, _ = _inputs(1, K * G, K, L, N, d)
+    b, e = _ranges(mask, 1, L, N)
+    want, lse = ops.httm_attention_forward(q, k, v, b, e)
+    lo, hi = b.clamp(0, N)[0], e.clamp(0, N)[0]
+    bad = {N - 1: float("nan"), N // 2: float("inf"), N // 3 + 1: -float("inf")}
+    v = v.clone()
+    for j, x in bad.items():
+        v[:, :, j, j % d] = x
+    out, lse2 = ops.httm_attention_forward(q, k, v, b, e)
+    assert torch.equal(lse, lse2)
+    for j, x in bad.items():
+        c, sees = j % d, (lo <= j) & (j < hi)
+        got = out[0, :, :, c].float()
+        assert torch.equal(got[:, ~sees], want[0, :, ~sees, c].float()), j
+        assert (torch.isnan(got[:, sees]) if x != x else got[:, sees] == x).all(), j
+    rest = torch.ones(d, dtype=torch.bool, device="cuda")
+    rest[[j % d for j in bad]] = False
+    assert torch.equal(out[..., rest], want[..., rest])
+    k = k.clone()
+    k[:, :, N - 1] = float("nan")
+    out, lse = ops.httm_attention_forward(q, k, v, b, e)
+    sees = (lo <= N - 1) & (N - 1 < hi)
+    assert torch.isnan(out[0, :, sees]).all() and torch.isnan(lse[0, :, sees]).all()
+    assert torch.equal(lse[0, :, ~sees], lse2[0, :, ~sees])
+    assert torch.equal(out[0][:, ~sees][..., rest], want[0][:, ~sees][..., rest])
+
+
 def test_far_offsets():
     """Batch entries more than 2^31 elements apart (a long cache)."""
     N, d = 200, 64

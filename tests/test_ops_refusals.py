@@ -39,6 +39,7 @@ def _forward(cfg=None, q=None, k=None, v=None, out=None, lse=FAKE, ws=FAKE, n=0,
     (dict(batch=-1), ARG), (dict(q_len=-1), ARG), (dict(kv_len=-2), ARG), (dict(heads=0), ARG), (dict(kv_heads=0), ARG),
     (dict(heads=5), ARG), (dict(d_head=0), ARG), (dict(dtype=7), ARG), (dict(softmax_scale=-1.0), ARG),
     (dict(softmax_scale=float("nan")), ARG), (dict(softmax_scale=float("inf")), ARG),
+    (dict(softmax_scale=1e-30), ARG), (dict(softmax_scale=1e30), ARG),
     (dict(dtype=1), UNSUPPORTED), (dict(d_head=72), UNSUPPORTED), (dict(d_head=12), UNSUPPORTED),
     (dict(q_len=(1 << 21) + 1), UNSUPPORTED), (dict(kv_len=(1 << 30) + 1), UNSUPPORTED),
     (dict(batch=40000), UNSUPPORTED), (dict(batch=1, heads=2000, kv_heads=1, q_len=1 << 21), UNSUPPORTED),

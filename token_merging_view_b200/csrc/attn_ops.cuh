@@ -63,6 +63,37 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int n, F&& dead) {
     }
 }
 
+// Is one of the two bf16 of x an infinity or NaN?
+__device__ __forceinline__ bool wild(uint32_t x) {
+  return (x & 0x7f800000u) == 0x7f800000u || (x & 0x7f80u) == 0x7f80u;
+}
+__device__ __forceinline__ bool wild(uint4 x) { return wild(x.x) || wild(x.y) || wild(x.z) || wild(x.w); }
+__device__ __forceinline__ uint32_t tame(uint32_t x) {
+  return ((x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u) | ((x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu);
+}
+// Does row r (128 bytes) of a swizzled tile hold infinities or NaN?
+// Neighbouring rows start at different 16-byte chunks, so a warp's accesses
+// meet no bank twice; an exponent of ones plus one carries into the sign bit.
+__device__ __forceinline__ bool wild_row(const uint8_t* tile, int r) {
+  const uint4* row = reinterpret_cast<const uint4*>(tile + r * 128);
+  uint32_t any = 0u;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 x = row[c ^ (r & 7)];
+    any |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+           ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+  }
+  return (any & 0x80008000u) != 0u;
+}
+// They become 0.
+__device__ __forceinline__ void tame_row(uint8_t* tile, int r) {
+  uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
+  for (int c = 0; c < 8; ++c) {
+    const uint4 x = row[c];
+    row[c] = make_uint4(tame(x.x), tame(x.y), tame(x.z), tame(x.w));
+  }
+}
+
 // Bounded wait that ignores the abort flag (to drain MMAs in flight).
 __device__ __forceinline__ void drain_mma(uint64_t* bar, uint32_t parity) {
   const WaitClock clk;

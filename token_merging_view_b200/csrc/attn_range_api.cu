@@ -33,7 +33,8 @@ httm_status check_attention(const httm_attention* a) {
   if (a->batch < 0 || a->q_len < 0 || a->kv_len < 0 || a->heads < 1 || a->kv_heads < 1) return HTTM_ERR_ARG;
   if (a->heads % a->kv_heads != 0 || a->d_head < 1) return HTTM_ERR_ARG;
   if (a->dtype != HTTM_BF16 && a->dtype != HTTM_F32) return HTTM_ERR_ARG;
-  if (!(a->softmax_scale >= 0.f) || !(a->softmax_scale - a->softmax_scale == 0.f)) return HTTM_ERR_ARG;
+  // 0 or within 2^-64 .. 2^64 (lse / scale has to stay finite)
+  if (!(a->softmax_scale == 0.f || (a->softmax_scale >= 0x1p-64f && a->softmax_scale <= 0x1p64f))) return HTTM_ERR_ARG;
   if (a->dtype != HTTM_BF16 || a->d_head % 8 != 0 || a->d_head > kAttnD) return HTTM_ERR_UNSUPPORTED;
   if (a->q_len > kAttnMaxQ || a->kv_len > (1 << 30)) return HTTM_ERR_UNSUPPORTED;
   const long long G = a->heads / a->kv_heads;

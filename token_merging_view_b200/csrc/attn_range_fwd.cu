@@ -27,7 +27,10 @@
 // Masks: a tile that every row of a warp sees whole takes no compares.
 // Keys outside the union of the item's ranges never enter: whole tiles are
 // not loaded, and in the last tile the V rows behind the union are zeroed
-// (a zero probability times a NaN there would not be zero).
+// (a zero probability times a NaN there would not be zero).  In a tile that
+// only some rows see, infinities and NaN in V are taken out before the
+// product and added at the end to the rows that see them, so that they reach
+// no other (the check costs such tiles about a tenth, other tiles nothing).
 #include <algorithm>
 #include <mutex>
 
@@ -51,12 +54,31 @@ struct FwdSmem {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t s_full[3], p_full[2], o_done[2];
   uint64_t drain, dirty, clean;
-  int lo[8], hi[8];
+  int lo[8], hi[8], f_lo[8], f_hi[8];
+  int wild;                              // V held infinities or NaN in a tile with masks
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kSmemBytes = sizeof(FwdSmem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Adds the infinities and NaN of the values [key, last) of a key head to an
+// output row in memory.
+template <class T>
+__device__ __noinline__ void add_wild(const AttnArgs& a, int b, int kh, int key, int last, T* row) {
+  for (; key < last; ++key) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.v.data) +
+                                                            b * a.v.sb + kh * a.v.sh + (int64_t)key * a.v.st);
+    for (int c = 0; c < a.d / 2; ++c) {
+      const uint32_t x = src[c];
+      if (!wild(x)) continue;
+      for (int e = 0; e < 2; ++e) {
+        const float v = __uint_as_float(e ? x & 0xffff0000u : x << 16);
+        if (!isfinite(v)) row[2 * c + e] = from_f<T>(to_f(row[2 * c + e]) + v);
+      }
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
 attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
@@ -83,9 +105,12 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
   if (warp >= 4) {
     const bool live = keys.x < keys.y;
     const int lo = warp_min(live ? keys.x : 0x7fffffff), hi = warp_max(live ? keys.y : 0);
+    const int f_lo = warp_max(live ? keys.x : 0), f_hi = warp_min(live ? keys.y : 0x7fffffff);
     if (lane == 0) {
       sm.lo[warp - 4] = lo;
       sm.hi[warp - 4] = hi;
+      sm.f_lo[warp - 4] = f_lo;
+      sm.f_hi[warp - 4] = f_hi;
     }
   }
   if (threadIdx.x == 0) {
@@ -103,6 +128,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
     mbar_init(&sm.dirty, 1);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
+    sm.wild = 0;
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
@@ -206,9 +232,13 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       const uint32_t to = tmem + lane_off + kColO + t * 64;      // this row of O_t
       const bool live = keys.x < keys.y;
       const bool warp_live = __any_sync(0xffffffffu, live);
-      // the warp's keys: some row sees [w_lo, w_hi), every live row [f_lo, f_hi)
+      // the warp's keys: some row sees [w_lo, w_hi), every live row [f_lo,
+      // f_hi); every live row of the tile [t_lo, t_hi)
+      // (warp reductions: the compiler knows their results to be uniform)
       const int w_lo = warp_min(live ? keys.x : 0x7fffffff) - base, w_hi = warp_max(live ? keys.y : 0) - base;
       const int f_lo = warp_max(live ? keys.x : 0) - base, f_hi = warp_min(live ? keys.y : 0x7fffffff) - base;
+      const int t_lo = warp_max(sm.f_lo[t * 4 + (lane & 3)]) - base;
+      const int t_hi = max(warp_min(sm.f_hi[t * 4 + (lane & 3)]), 0) - base;
       // the row's queries into the swizzled tile (zeros behind d, and for
       // rows that see nothing, whatever memory holds there)
       {
@@ -234,6 +264,22 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
         tc_fence_after();
         const int k0 = j * kAttnTile;                            // the tile's keys, counted from base
         bool pv_done = j == 0;                                   // PV(t, j-1) seen complete
+        if (t_lo > k0 || t_hi < min(k0 + kAttnTile, hi - base)) {
+          // some row does not see all that others see of this tile, and its
+          // zero probability times an infinity or NaN there would not be
+          // zero: those elements leave V (one row a thread) and reach the
+          // rows that do see them at the end
+          const int s = j % kStages;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], (j / kStages) & 1, abort, st))) { ok = false; break; }
+          if (wild_row(sm.v[s], row)) {
+            // tile 0's product with this V comes first and takes it as it
+            // is; tile 1's comes behind both tiles' P, so it sees the note
+            if (t == 1) mbar_wait(&sm.o_done[0], j & 1, abort, st);
+            sm.wild = 1;
+            tame_row(sm.v[s], row);
+            fence_async_smem();
+          }
+        }
         if (w_lo >= k0 + kAttnTile || w_hi <= k0) {
           // none of this warp's rows sees this tile: P = 0 (rows that are
           // never stored may keep what is there)
@@ -294,7 +340,8 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 64; ++e)
               mx[e & 3] = max3(mx[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-            const float m_new = fmaxf(m_used, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale_log2);
+            // a row that did not ask keeps its reference, and so its bits
+            const float m_new = need ? fmaxf(m_used, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale_log2) : m_used;
             // a row with nothing yet: reference 0, its P and sum stay 0
             m_ref = m_new == -INFINITY ? 0.f : m_new;
             const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_ref);
@@ -335,6 +382,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       if (ok && n_kv > 0)
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], (n_kv - 1) & 1, abort, st));
       tc_fence_after();
+      const int wild_end = sm.wild && live ? min(keys.y, base + n_kv * kAttnTile) : 0;
       if (ok && parts > 1) {
         // unnormalised sums, the row sum and the maximum in use; rows are
         // counted without the padding of a last tile
@@ -354,6 +402,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
         if (in_item) {
           dst[kAttnD] = sum;
           dst[kAttnD + 1] = m_used;
+          if (wild_end) add_wild(a, b, kh, max(keys.x, base), wild_end, dst);
         }
       } else if (ok) {
         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + head * a.out.sh +
@@ -363,6 +412,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
           tmem_ld64(to, o);
           if (in_item && live) store_row_bf16<8>(o, dst, 1.f / sum, 0, a.d);
         }
+        if (wild_end) add_wild(a, b, kh, max(keys.x, base), wild_end, dst);
         if (in_item && !live)
           for (int v = 0; v < a.d / 8; ++v) reinterpret_cast<uint4*>(dst)[v] = make_uint4(0, 0, 0, 0);
         if (in_item && a.lse)

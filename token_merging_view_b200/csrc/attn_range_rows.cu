@@ -177,6 +177,13 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
       __syncwarp();
     }
     const bool masked = k0 < f_lo || k0 + kKeys > f_hi;
+    // a zero probability times an infinity or NaN is not zero: where a row
+    // does not see the whole tile, such elements leave V (a row a lane) and
+    // are added below to the rows that see them
+    const bool mixed = k0 < f_lo || min(k0 + kKeys, hi) > f_hi;
+    const uint32_t odd = mixed ? __ballot_sync(0xffffffffu, wild_row(vs, lane)) : 0u;
+    if (odd >> lane & 1) tame_row(vs, lane);
+    __syncwarp();
     const uint32_t ka = smem_u32(ks), va = smem_u32(vs);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -248,6 +255,26 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
           mma16(o[t][2 * j], p, x[0], x[1]);
           mma16(o[t][2 * j + 1], p, x[2], x[3]);
         }
+      }
+    }
+    for (uint32_t rest = odd; rest; rest &= rest - 1) {
+      const int key = k0 + __ffs(rest) - 1;
+      const __nv_bfloat16* src =
+          reinterpret_cast<const __nv_bfloat16*>(a.v.data) + b * a.v.sb + kh * a.v.sh + (int64_t)key * a.v.st;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = j * 8 + c0;
+        if (key >= a.N || c >= a.d) continue;
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(src + c);
+        if (!wild(x)) continue;
+        const float v[2] = {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int2 kr = keys[t][e >> 1];
+            if (key >= kr.x && key < kr.y && !isfinite(v[e & 1])) o[t][j][e] += v[e & 1];
+          }
       }
     }
     __syncwarp();
