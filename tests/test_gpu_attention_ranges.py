@@ -88,6 +88,12 @@ CASES = [
     (1, 2, 2, 700, 300, 64, "none"),           # more queries than keys
     (1, 1, 1, 1500, 1500, 64, "none"),         # queries of a key tile split
     (1, 2, 1, 513, 130, 64, "random"),
+    # long enough for two groups of warps a block in dK/dV, dQ, or both
+    (1, 2, 1, 1300, 1300, 64, "causal"),
+    (1, 1, 1, 2500, 2500, 64, "window"),
+    (2, 2, 2, 700, 3001, 40, "random"),
+    (2, 4, 2, 1201, 3300, 64, "padded"),
+    (1, 1, 1, 3500, 3500, 64, "packed"),
     # few rows a key head: one, 16, 17, 32 and (past them) 33
     (1, 1, 1, 1, 31, 64, "none"),
     (3, 16, 1, 1, 700, 64, "padded"),
@@ -169,12 +175,13 @@ def test_broadcast_inputs():
         assert torch.equal(got[n], want[n]), n
 
 
-def test_unseen_places_may_hold_anything():
+@pytest.mark.parametrize("H,L,N", [(4, 150, 300), (32, 150, 4000)])
+def test_unseen_places_may_hold_anything(H, L, N):
     """NaN and infinities in keys and values nobody sees, and in queries,
     outputs and output gradients of rows that see nothing, change no bit."""
-    B, H, K, L, N, d = 3, 4, 2, 150, 300, 64
+    B, K, d = 3, 2, 64
     q, k, v, dout = _inputs(B, H, K, L, N, d)
-    n = torch.tensor([300, 129, 0], device="cuda")
+    n = torch.tensor([N, 129, 0], device="cuda")
     b, e = ops.length_ranges(n, L)
     b = b + torch.tensor([17, 0, 0], device="cuda", dtype=torch.int32)[:, None]
     e[1, 40:60] = 0

@@ -7,7 +7,6 @@
 namespace httm {
 
 constexpr int kAttnTile = 128;          // keys, or query rows, of one tensor-core tile
-constexpr int kAttnStep = 96;           // queries (dK, dV) or keys (dQ) of one step of the backward kernels
 constexpr int kAttnD = 64;              // channels of a tile; narrower heads are padded with zeros
 constexpr int kAttnMaxQ = 1 << 21;      // queries of one sequence
 constexpr int kAttnMaxParts = 64;       // key splits of one forward work item
@@ -61,7 +60,8 @@ struct AttnTileRange {
   int pad[3];
 };
 struct AttnBwdPlan {
-  int q_tiles, k_tiles, Lp;             // tiles of kAttnStep queries, of 128 keys; Lp: rows kept per head
+  int kv_groups, q_groups;              // groups a block of the two kernels (1 or 2)
+  int step, q_tiles, k_tiles, Lp;       // tiles of `step` queries, of 128 keys; Lp: rows kept per head
   int kv_parts;                         // splits of the queries of one key tile
   size_t stat, extra, range, tiles, part, total;
 };

@@ -23,20 +23,20 @@
 // key-owning CTAs needs either atomics, whose order would change the result
 // from run to run, or N x N / 128 partial sums.
 //
-// Both kernels move in steps of 96 (queries, or keys for dQ): two groups of
-// warps take the even and the odd steps, each with its own S and dP in TMEM
-// (2 x 2 x 96 columns; the accumulators take the other 128), so that one
-// group exponentiates while the other forms dS, and neither waits for a
-// buffer of the other.  P overwrites its S and dS its dP, as bf16 pairs.
+// Both kernels are made of groups: two warpgroups of 4 warps (TMEM lane =
+// row, each with half of the columns) with an S and a dP of their own in
+// TMEM, so that one group exponentiates while another forms dS and neither
+// waits for the other's buffer.  P overwrites its S and dS its dP, as bf16
+// pairs.  Short sequences run two blocks of one group an SM, long ones a
+// block of two groups that take the even and the odd steps (Cfg).
 // Warp 0 loads (TMA); one thread of warp 1 and one of warp 3 issue the MMAs:
 // one alone issues an N = 64 product at half the tensor core's rate, two
 // keep it fed.  They share the work so that a product which overwrites an
 // operand is issued by the thread that issued that operand's use (the tensor
 // core works in order of issue per thread), and so that every accumulator
 // has one issuing thread: its order of summation is fixed.  For dK and dV
-// warp 1 has S and dV, warp 3 dP and dK; for dQ each has a group, with an
-// accumulator of its own.  Warp 2 clears loaded rows that may hold anything.  A group is kHalves warpgroups of 4 warps (TMEM lane = row),
-// each with 96 / kHalves of the columns.
+// warp 1 has S and dV, warp 3 dP and dK; for dQ each group has its issuing
+// warp and an accumulator.  Warp 2 clears loaded rows that may hold anything.
 //
 // Parity waits: a barrier of a group completes one phase per step of that
 // group, and no phase can begin before every waiter has seen the one before:
@@ -51,25 +51,31 @@ namespace {
 
 using namespace tc;
 
-constexpr int kStages = 5;                            // query tiles in flight (dK, dV)
-constexpr int kKvStages = 6;                          // key tiles in flight (dQ)
-constexpr int kStep = kAttnStep;
-constexpr int kHalves = 2;                            // warpgroups of a group
-constexpr int kCols = kStep / kHalves;                // columns of a thread
+// G groups a block (see above): 1 with two blocks an SM, 2 with one.
+template <int G>
+struct Cfg {
+  static constexpr int kThreads = 128 + 256 * G, kBlocks = 3 - G;
+  static constexpr uint32_t kTmem = 256 * G;          // tensor memory columns
+  // registers a thread: launched at 80 or 96, then 128 kAuxRegs + 256 G
+  // kWorkRegs of the same total
+  static constexpr int kLaunchRegs = G == 1 ? 80 : 96, kAuxRegs = G == 1 ? 48 : 64, kWorkRegs = G == 1 ? 96 : 104;
+  static_assert(128 * kAuxRegs + 256 * G * kWorkRegs <= kThreads * kLaunchRegs, "registers");
+  static_assert(kBlocks * kThreads * kLaunchRegs <= 65536, "registers");
+  // dK, dV: queries of a step, columns of a thread, query tiles in flight
+  static constexpr int kStep = G == 1 ? 64 : 96, kCols = kStep / 2, kStages = G == 1 ? 3 : 5;
+  static constexpr uint32_t kStepBytes = kStep * kAttnD * 2;
+  static constexpr uint32_t kColV = G * 2 * kStep, kColK = kColV + kAttnD;   // group g: S at 2 g kStep, dP kStep behind
+  // dQ: the same for keys
+  static constexpr int kKeyStep = 96, kKeyCols = kKeyStep / 2, kKvStages = 3 * G;
+  static constexpr uint32_t kKeyBytes = kKeyStep * kAttnD * 2;
+  static constexpr uint32_t kColQ = G * 2 * kKeyStep;                        // group g's dQ at kColQ + 64 g
+  static_assert(kColK + kAttnD <= kTmem && kColQ + G * kAttnD <= kTmem, "tensor memory");
+  static_assert(kStepBytes % 1024 == 0 && kKeyBytes % 1024 == 0, "tiles start on 1024 bytes");
+};
+constexpr int kMaxQTiles = kAttnMaxQ / 64;
+constexpr int kMaxWords = kMaxQTiles / 32;
 constexpr int kChunk = 16;                            // columns in registers at a time
-constexpr int kGroupThreads = kHalves * 128;
-constexpr int kThreads = 128 + 2 * kGroupThreads;
-// registers a thread: launched at 65,536 / kThreads (a multiple of 8), then
-// 128 kAuxRegs + 2 kGroupThreads kWorkRegs of the same total
-constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-constexpr int kWorkRegs = kHalves == 2 ? 104 : 208, kAuxRegs = kHalves == 2 ? 64 : 88;
-static_assert(128 * kAuxRegs + 2 * kGroupThreads * kWorkRegs <= kThreads * kLaunchRegs, "registers");
-constexpr uint32_t kStepBytes = kStep * kAttnD * 2;   // 12 KB
-constexpr int kMaxQTiles = (kAttnMaxQ + kStep - 1) / kStep;
-constexpr int kMaxWords = (kMaxQTiles + 31) / 32;
-constexpr uint32_t kColA = 384, kColB = 448;          // accumulators: dV and dK, or the two groups' dQ
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kCols % kChunk == 0 && kCols % 16 == 0, "whole chunks, whole K steps");
 
 // ------------------------------------------------------------------ prep
 // x as the sum of three bf16 (24 bits: all of an fp32), and five zeros.
@@ -78,7 +84,8 @@ __device__ __forceinline__ uint4 three_bf16(float x) {
   return make_uint4(pack_bf16(hi, mid), pack_bf16(x - hi - mid, 0.f), 0u, 0u);
 }
 
-// One step's 96 rows of one head a block, 8 threads a row.
+// One step's rows of one head a block, 8 threads a row.
+template <int kStep>
 __global__ void __launch_bounds__(256)
 attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restrict__ nlse, float* __restrict__ ndsum,
                  uint4* __restrict__ extra, int2* __restrict__ ranges, AttnTileRange* __restrict__ tiles) {
@@ -148,21 +155,22 @@ attn_prep_kernel(const __grid_constant__ AttnArgs a, int q_tiles, float* __restr
 // addresses in 16-byte units stay below the field's 14 bits).
 __device__ __forceinline__ uint64_t tile_desc(const uint8_t* tile) { return sw128_desc(smem_u32(tile), 1024); }
 
-// D (+)= A B^T: K-major tiles of 128 and of 96 rows x 64 channels.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t A, uint64_t B, bool add = false) {
-  constexpr uint32_t id = idesc_bf16(128, kStep, false, false);
+// D (+)= A B^T: K-major tiles of 128 and of N rows x 64 channels.
+template <int N>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t A, uint64_t B, bool add) {
+  constexpr uint32_t id = idesc_bf16(128, N, false, false);
 #pragma unroll
   for (int kk = 0; kk < kAttnD / 16; ++kk) umma_bf16(d, A + kk * 2, B + kk * 2, id, (add || kk > 0) ? 1u : 0u);
 }
-// D (+)= A B: A the 128 x 96 P or dS that the warpgroups of a group wrote to
-// the front of their columns of the product at `A`; B a tile of 96 rows x 64
-// channels.
+// D (+)= A B: A the 128 x N P or dS that the two warpgroups wrote to the front
+// of their halves of the product at `A`; B a tile of N rows x 64 channels.
+template <int N>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t A, uint64_t B, bool add) {
   constexpr uint32_t id = idesc_bf16(128, kAttnD, false, true);
-  constexpr int per = kCols / 16;                     // K steps of one warpgroup's columns
+  constexpr int per = N / 32;                         // K steps of one warpgroup's columns
 #pragma unroll
-  for (int kk = 0; kk < kStep / 16; ++kk)
-    umma_bf16_ts(d, A + (kk / per) * kCols + (kk % per) * 8, B + kk * 128, id, (add || kk > 0) ? 1u : 0u);
+  for (int kk = 0; kk < N / 16; ++kk)
+    umma_bf16_ts(d, A + (kk / per) * (N / 2) + (kk % per) * 8, B + kk * 128, id, (add || kk > 0) ? 1u : 0u);
 }
 
 // Two neighbouring scores: s -> 2^(s c + m), or 2^(s c).
@@ -194,7 +202,9 @@ __device__ __forceinline__ uint32_t ds_pair(uint32_t p0, uint32_t p1, uint32_t g
 }
 
 // ------------------------------------------------------------------ dK, dV
+template <int G>
 struct DkvSmem {
+  static constexpr int kStages = Cfg<G>::kStages, kStep = Cfg<G>::kStep, kStepBytes = Cfg<G>::kStepBytes;
   uint8_t k[kTileBytes], v[kTileBytes];
   uint8_t q[kStages][kStepBytes], g[kStages][kStepBytes];     // query and dout tiles
   uint4 ones[2][kAttnTile];                                   // K = 16 operand: 1 1 1 0 0 0 0 0, and zeros
@@ -204,15 +214,15 @@ struct DkvSmem {
   int flags[kStages];                                         // kMasked, kDead of the step in each stage
   uint32_t active[kMaxWords], masked[kMaxWords], dead[kMaxWords];
   uint64_t kv_full, q_full[kStages], q_empty[kStages];
-  uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2], drain, dirty, clean;
-  int count[kThreads / 32];
+  uint64_t s_full[G], dp_full[G], p_ready[G], ds_ready[G], drain, dirty, clean;
+  int count[Cfg<G>::kThreads / 32];
   uint32_t tmem_base;
   int abort;
 };
 constexpr int kMasked = 1, kDead = 2;
-constexpr size_t kDkvSmem = sizeof(DkvSmem) + 1024;
-static_assert(kDkvSmem <= 227 * 1024, "shared memory");
-static_assert(kStepBytes % 1024 == 0, "tiles start on 1024 bytes");
+template <int G>
+constexpr size_t kDkvSmem = sizeof(DkvSmem<G>) + 1024;
+static_assert(2 * (kDkvSmem<1> + 1024) <= 227 * 1024 && kDkvSmem<2> <= 226 * 1024, "shared memory");
 
 // Walks over the set bits of `active`, round after round (one per head).
 struct TileWalk {
@@ -247,14 +257,18 @@ struct TileWalk {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int G>
+__global__ void __launch_bounds__(Cfg<G>::kThreads, Cfg<G>::kBlocks)
 attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
                 const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
                 const __grid_constant__ AttnArgs a, int q_tiles, int k_tiles, int parts,
                 const uint4* __restrict__ extra, const int2* __restrict__ ranges,
                 const AttnTileRange* __restrict__ tiles, float* __restrict__ part_out) {
+  using C = Cfg<G>;
+  constexpr int kStep = C::kStep, kCols = C::kCols, kStages = C::kStages, kThreads = C::kThreads;
+  constexpr uint32_t kStepBytes = C::kStepBytes;
   extern __shared__ uint8_t smem_raw[];
-  DkvSmem& sm = *reinterpret_cast<DkvSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DkvSmem<G>& sm = *reinterpret_cast<DkvSmem<G>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const unsigned item = blockIdx.x / parts, part = blockIdx.x % parts;
   const int bk = item / k_tiles, kt = item % k_tiles, b = bk / a.K, kh = bk % a.K;
@@ -297,11 +311,11 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.dp_full[i], 1);
-      mbar_init(&sm.p_ready[i], kGroupThreads);
-      mbar_init(&sm.ds_ready[i], kGroupThreads);
+    for (int g = 0; g < G; ++g) {
+      mbar_init(&sm.s_full[g], 1);
+      mbar_init(&sm.dp_full[g], 1);
+      mbar_init(&sm.p_ready[g], 256);
+      mbar_init(&sm.ds_ready[g], 256);
     }
     mbar_init(&sm.drain, 2);
     mbar_init(&sm.dirty, 2);
@@ -309,7 +323,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
     sm.abort = 0;
     mbar_fence_init();
   }
-  if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 0) tmem_alloc(&sm.tmem_base, C::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -322,7 +336,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
   const int s0 = (int)(all * part / parts), n = uniform((int)(all * (part + 1) / parts) - s0);   // steps of this CTA
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs) : "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs) : "memory");
     if (warp == 0 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ producer
       mbar_arrive_expect_tx(&sm.kv_full, 2 * kTileBytes);
@@ -350,7 +364,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       constexpr uint32_t id = idesc_bf16(128, kStep, false, false);
       const uint64_t one = plain_desc(smem_u32(sm.ones), kAttnTile * 16, 128);
       const uint32_t ext0 = smem_u32(sm.extra[0][first ? 0 : 1]), zeros = smem_u32(sm.zeros);
-      const uint32_t buf = tmem + (first ? 0 : kStep), acc = tmem + (first ? kColA : kColB);
+      const uint32_t buf = tmem + (first ? 0 : kStep), acc = tmem + (first ? C::kColV : C::kColK);
       uint64_t* full = first ? sm.s_full : sm.dp_full;
       uint64_t* ready = first ? sm.p_ready : sm.ds_ready;
       int n_dirty = 0;
@@ -365,41 +379,41 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
         return true;
       };
       // operands of product i (outside the elected branch: they stay uniform)
-      auto dest = [&](int i) { return buf + (i & 1) * 2 * kStep; };
       auto row_desc = [&](int i) { return rows + (i % kStages) * (kStepBytes >> 4); };
       auto ext_desc = [&](int i) {
         const uint32_t ext = ext0 + (i % kStages) * (kStep * 32);
         return plain_desc(ext, zeros - ext, 128);
       };
+      auto dest = [&](int i) { return buf + (i % G) * 2 * kStep; };
       bool ok = wait_all(&sm.kv_full, 0, abort, st);
-      for (int i = 0; ok && i < min(2, n); ++i) {
+      for (int i = 0; ok && i < min(G, n); ++i) {
         if (!(ok = loaded(i))) break;
         tc_fence_after();
         const uint64_t rd = row_desc(i), ed = ext_desc(i);
         const uint32_t d = dest(i);
         if (elect_one()) {
           umma_bf16(d, one, ed, id, 0u);
-          mma_rows(d, own, rd, true);
-          umma_commit(&full[i & 1]);
+          mma_rows<kStep>(d, own, rd, true);
+          umma_commit(&full[i % G]);
         }
         __syncwarp();
       }
       // what the next product needs is waited for first, so that it follows
       // the P (dS) it overwrites at once
       for (int i = 0; ok && i < n; ++i) {
-        const int s = i % kStages, grp = i & 1;
-        const bool more = i + 2 < n;
-        if (more && !loaded(i + 2)) break;
-        const uint64_t rd = row_desc(i + 2), ed = ext_desc(i + 2), cd = cols + s * (kStepBytes >> 4);
+        const int s = i % kStages, grp = i % G;
+        const bool more = i + G < n;
+        if (more && !loaded(i + G)) break;
+        const uint64_t rd = row_desc(i + G), ed = ext_desc(i + G), cd = cols + s * (kStepBytes >> 4);
         const uint32_t d = dest(i);
-        if (!wait_all(&ready[grp], (i >> 1) & 1, abort, st)) break;
+        if (!wait_all(&ready[grp], (i / G) & 1, abort, st)) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_cols(acc, d, cd, i > 0);
+          mma_cols<kStep>(acc, d, cd, i > 0);
           umma_commit(&sm.q_empty[s]);
           if (more) {
             umma_bf16(d, one, ed, id, 0u);
-            mma_rows(d, own, rd, true);
+            mma_rows<kStep>(d, own, rd, true);
             umma_commit(&full[grp]);
           }
         }
@@ -429,103 +443,102 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegs) : "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWorkRegs) : "memory");
     // ------------------------------------------------------------ P and dS
-    const int grp = (warp - 4) / (4 * kHalves), half = ((warp - 4) >> 2) % kHalves, row = (warp & 3) * 32 + lane;
+    const int wg = (warp - 4) >> 2, grp = wg >> 1, half = wg & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_off + grp * 2 * kStep + half * kCols, td = ts + kStep;
     const int key = k0 + row;
     const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2);
     bool ok = true;
-    if (n > grp) {
-      for (int i = grp; i < n; i += 2) {
-        const int s = i % kStages, m = i >> 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) ||
-            !__all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], m & 1, abort, st))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool masked = __any_sync(0xffffffffu, sm.flags[s] & kMasked);
-        // p = 2^(c (s - lse / scale)) of this key and the queries of the columns
-        uint32_t p[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < kCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc);
-        if (masked) {
-          const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + half * kCols);
-#pragma unroll
-          for (int e = 0; e < kCols / 2; ++e) {
-            const int4 r = rp[e];
-            if (key < r.x || key >= r.y) p[2 * e] = 0u;
-            if (key < r.z || key >= r.w) p[2 * e + 1] = 0u;
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < kCols; c += kChunk) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            pk[e] = pack_bf16(__uint_as_float(p[c + 2 * e]), __uint_as_float(p[c + 2 * e + 1]));
-          tmem_st8(ts + c / 2, pk);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sm.p_ready[grp]);
-        // dS = P (dP - D)
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.dp_full[grp], m & 1, abort, st))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < kCols; c += kChunk) {
-          uint32_t g[16], pk[8];
-          tmem_ld16(td + c, g);
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (p[c + e] == 0u) g[e] = 0u;                    // a value nobody sees may be NaN
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pk[e] = mul_pair(p[c + 2 * e], p[c + 2 * e + 1], g[2 * e], g[2 * e + 1]);
-          tmem_st8(td + c / 2, pk);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sm.ds_ready[grp]);
+    for (int i = grp; i < n; i += G) {
+      const int s = i % kStages, m = i / G;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[s], (i / kStages) & 1, abort, st)) ||
+          !__all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], m & 1, abort, st))) {
+        ok = false;
+        break;
       }
+      tc_fence_after();
+      const bool masked = __any_sync(0xffffffffu, sm.flags[s] & kMasked);
+      // p = 2^(c (s - lse / scale)) of this key and the queries of the columns
+      uint32_t p[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < kCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc);
+      if (masked) {
+        const int4* rp = reinterpret_cast<const int4*>(sm.range[s] + half * kCols);
+#pragma unroll
+        for (int e = 0; e < kCols / 2; ++e) {
+          const int4 r = rp[e];
+          if (key < r.x || key >= r.y) p[2 * e] = 0u;
+          if (key < r.z || key >= r.w) p[2 * e + 1] = 0u;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kCols; c += kChunk) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          pk[e] = pack_bf16(__uint_as_float(p[c + 2 * e]), __uint_as_float(p[c + 2 * e + 1]));
+        tmem_st8(ts + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sm.p_ready[grp]);
+      // dS = P (dP - D)
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.dp_full[grp], m & 1, abort, st))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kCols; c += kChunk) {
+        uint32_t g[16], pk[8];
+        tmem_ld16(td + c, g);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (p[c + e] == 0u) g[e] = 0u;                    // a value nobody sees may be NaN
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = mul_pair(p[c + 2 * e], p[c + 2 * e + 1], g[2 * e], g[2 * e + 1]);
+        tmem_st8(td + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sm.ds_ready[grp]);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
     tc_fence_after();
-    // the first group stores dV, the second dK; each warpgroup its channels
+    // the first half of the warpgroups store dV, the others dK
     if (ok) {
-      constexpr int kOut = kAttnD / kHalves;
+      constexpr int kOut = kAttnD / G;                          // channels of a warpgroup
+      const int which = wg / G, o0 = wg % G * kOut;
       uint32_t o[kOut];
       if (n > 0) {
+        const uint32_t src = tmem + lane_off + (which == 0 ? C::kColV : C::kColK) + o0;
 #pragma unroll
-        for (int c = 0; c < kOut; c += 16)
-          tmem_ld16(tmem + lane_off + (grp == 0 ? kColA : kColB) + half * kOut + c, *reinterpret_cast<uint32_t(*)[16]>(&o[c]));
+        for (int c = 0; c < kOut; c += 32) tmem_ld32(src + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
         tmem_wait_ld();
       } else {
 #pragma unroll
         for (int e = 0; e < kOut; ++e) o[e] = 0u;
       }
       if (parts > 1) {
-        float4* dst = reinterpret_cast<float4*>(part_out + (((size_t)blockIdx.x * 2 + grp) * kAttnTile + row) * kAttnD +
-                                                half * kOut);
+        float4* dst =
+            reinterpret_cast<float4*>(part_out + (((size_t)blockIdx.x * 2 + which) * kAttnTile + row) * kAttnD + o0);
 #pragma unroll
         for (int v = 0; v < kOut / 4; ++v)
           dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]), __uint_as_float(o[4 * v + 2]),
                                __uint_as_float(o[4 * v + 3]));
       } else if (key < a.N) {
-        const View& w = grp == 0 ? a.dv : a.dk;
+        const View& w = which == 0 ? a.dv : a.dk;
         __nv_bfloat16* dst =
             reinterpret_cast<__nv_bfloat16*>(w.data) + b * w.sb + kh * w.sh + (int64_t)key * w.st;
-        store_row_bf16<kOut / 8>(o, dst, grp == 0 ? 1.f : a.scale, half * kOut, a.d);
+        store_row_bf16<kOut / 8>(o, dst, which == 0 ? 1.f : a.scale, o0, a.d);
       }
     }
   }
@@ -536,7 +549,7 @@ attn_dkv_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ Attn
     if (*abort)
       for (int i = 0; i < 200; ++i) __nanosleep(1000);           // copies in flight land
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -567,34 +580,40 @@ attn_dkv_join_kernel(const __grid_constant__ AttnArgs a, int k_tiles, int parts,
 }
 
 // ------------------------------------------------------------------ dQ
+template <int G>
 struct DqSmem {
+  static constexpr int kKvStages = Cfg<G>::kKvStages, kKeyBytes = Cfg<G>::kKeyBytes;
   uint8_t q[kTileBytes], g[kTileBytes];
-  uint8_t k[kKvStages][kStepBytes], v[kKvStages][kStepBytes];
+  uint8_t k[kKvStages][kKeyBytes], v[kKvStages][kKeyBytes];
   uint64_t q_full, kv_full[kKvStages], kv_empty[kKvStages];
-  uint64_t s_full[2], dp_full[2], s_read[2], ds_ready[2], drain, dirty, clean;
+  uint64_t s_full[G], dp_full[G], s_read[G], ds_ready[G], drain, dirty, clean;
   int lo[4], hi[4];
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kDqSmem = sizeof(DqSmem) + 1024;
-static_assert(kDqSmem <= 227 * 1024, "shared memory");
+template <int G>
+constexpr size_t kDqSmem = sizeof(DqSmem<G>) + 1024;
+static_assert(2 * (kDqSmem<1> + 1024) <= 227 * 1024 && kDqSmem<2> <= 226 * 1024, "shared memory");
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int G>
+__global__ void __launch_bounds__(Cfg<G>::kThreads, Cfg<G>::kBlocks)
 attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnMap mg,
                const __grid_constant__ AttnMap mk, const __grid_constant__ AttnMap mv,
-               const __grid_constant__ AttnArgs a, int q_tiles, const float* __restrict__ nlse,
+               const __grid_constant__ AttnArgs a, int Lp, const float* __restrict__ nlse,
                const float* __restrict__ ndsum, const int2* __restrict__ ranges) {
+  using C = Cfg<G>;
+  constexpr int kKeyStep = C::kKeyStep, kKeyCols = C::kKeyCols, kKvStages = C::kKvStages;
+  constexpr uint32_t kKeyBytes = C::kKeyBytes;
   extern __shared__ uint8_t smem_raw[];
-  DqSmem& sm = *reinterpret_cast<DqSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DqSmem<G>& sm = *reinterpret_cast<DqSmem<G>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int m_tiles = (a.L + kAttnTile - 1) / kAttnTile;        // tiles of 128 queries; later ones first
   const int bh = blockIdx.x / m_tiles, qt = m_tiles - 1 - blockIdx.x % m_tiles;
   const int b = bh / a.H, h = bh % a.H, kh = h / a.G;
-  const size_t Lp = (size_t)q_tiles * kStep;
   // this thread's query and its keys; the union of the tile's
-  const int half = ((warp - 4) >> 2) % kHalves, grp = (warp - 4) / (4 * kHalves);
+  const int wg = (warp - 4) >> 2, grp = wg >> 1, half = wg & 1;
   const int row = (warp & 3) * 32 + lane, l = qt * kAttnTile + row;
-  const int2 keys = warp >= 4 && l < a.L ? ranges[b * Lp + l] : make_int2(0, 0);
+  const int2 keys = warp >= 4 && l < a.L ? ranges[(size_t)b * Lp + l] : make_int2(0, 0);
   const bool live = keys.x < keys.y;
   if (warp >= 4 && warp < 8) {
     const int x = warp_min(live ? keys.x : 0x7fffffff), y = warp_max(live ? keys.y : 0);
@@ -611,19 +630,19 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.dp_full[i], 1);
-      mbar_init(&sm.s_read[i], kGroupThreads);
-      mbar_init(&sm.ds_ready[i], kGroupThreads);
+    for (int g = 0; g < G; ++g) {
+      mbar_init(&sm.s_full[g], 1);
+      mbar_init(&sm.dp_full[g], 1);
+      mbar_init(&sm.s_read[g], 256);
+      mbar_init(&sm.ds_ready[g], 256);
     }
-    mbar_init(&sm.drain, 2);
+    mbar_init(&sm.drain, G);
     mbar_init(&sm.dirty, 1);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
     mbar_fence_init();
   }
-  if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 0) tmem_alloc(&sm.tmem_base, C::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -631,11 +650,11 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
   volatile int* abort = &sm.abort;
   const int lo = min(min(sm.lo[0], sm.lo[1]), min(sm.lo[2], sm.lo[3]));
   const int hi = max(max(sm.hi[0], sm.hi[1]), max(sm.hi[2], sm.hi[3]));
-  const int n = uniform(lo < hi ? (hi - lo + kStep - 1) / kStep : 0), base = n > 0 ? lo : 0;
-  const int n_last = hi - (base + (n - 1) * kStep);             // keys of the union in the last step
+  const int n = uniform(lo < hi ? (hi - lo + kKeyStep - 1) / kKeyStep : 0), base = n > 0 ? lo : 0;
+  const int n_last = hi - (base + (n - 1) * kKeyStep);             // keys of the union in the last step
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs) : "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs) : "memory");
     if (warp == 0 && lane == 0 && n > 0) {
       // ------------------------------------------------------------ producer
       mbar_arrive_expect_tx(&sm.q_full, 2 * kTileBytes);
@@ -644,22 +663,21 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       for (int j = 0; j < n; ++j) {
         const int s = j % kKvStages;
         if (j >= kKvStages && !mbar_wait(&sm.kv_empty[s], ((j / kKvStages) - 1) & 1, abort, st)) break;
-        mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kStepBytes);
-        tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kStep, kh, b);
-        tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kStep, kh, b);
+        mbar_arrive_expect_tx(&sm.kv_full[s], 2 * kKeyBytes);
+        tma_load_tile(sm.k[s], mk, &sm.kv_full[s], base + j * kKeyStep, kh, b);
+        tma_load_tile(sm.v[s], mv, &sm.kv_full[s], base + j * kKeyStep, kh, b);
       }
-    } else if ((warp == 1 || warp == 3) && n > 0) {
+    } else if ((warp == 1 || (G == 2 && warp == 3)) && n > 0) {
       // ------------------------------------------------------------ MMA issue
-      // warp 1 for the first group, warp 3 for the second: S = Q K^T, dP = dO
-      // V^T, dQ_g += dS K, each group with its own accumulator
+      // a warp a group: S = Q K^T, dP = dO V^T, dQ_g += dS K
       const int g = warp >> 1;
       const uint64_t qd = tile_desc(sm.q), gd = tile_desc(sm.g), kd = tile_desc(sm.k[0]), vd = tile_desc(sm.v[0]);
-      const uint32_t buf = tmem + g * 2 * kStep, acc = tmem + (g ? kColB : kColA);
+      const uint32_t buf = tmem + g * 2 * kKeyStep, acc = tmem + C::kColQ + g * kAttnD;
       // waits for the tiles of step j; the last one's K rows behind the union are cleared
       auto loaded = [&](int j) -> bool {
         const int s = j % kKvStages;
         if (!wait_all(&sm.kv_full[s], (j / kKvStages) & 1, abort, st)) return false;
-        if (j == n - 1 && n_last < kStep) {
+        if (j == n - 1 && n_last < kKeyStep) {
           if (lane == 0) mbar_arrive(&sm.dirty);
           if (!wait_all(&sm.clean, 0, abort, st)) return false;
         }
@@ -668,25 +686,25 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       bool ok = g < n && wait_all(&sm.q_full, 0, abort, st) && loaded(g);
       if (ok) {
         tc_fence_after();
-        const uint64_t k1 = kd + g * (kStepBytes >> 4), v1 = vd + g * (kStepBytes >> 4);
+        const uint64_t k1 = kd + g * (kKeyBytes >> 4), v1 = vd + g * (kKeyBytes >> 4);
         if (elect_one()) {
-          mma_rows(buf, qd, k1);
+          mma_rows<kKeyStep>(buf, qd, k1, false);
           umma_commit(&sm.s_full[g]);
-          mma_rows(buf + kStep, gd, v1);
+          mma_rows<kKeyStep>(buf + kKeyStep, gd, v1, false);
           umma_commit(&sm.dp_full[g]);
         }
         __syncwarp();
       }
-      for (int j = g; ok && j < n; j += 2) {
-        const int m = j >> 1, s = j % kKvStages, s2 = (j + 2) % kKvStages;
-        const bool more = j + 2 < n;
+      for (int j = g; ok && j < n; j += G) {
+        const int m = j / G, s = j % kKvStages, s2 = (j + G) % kKvStages;
+        const bool more = j + G < n;
         // operands outside the elected branches: they stay uniform
-        const uint64_t k0 = kd + s * (kStepBytes >> 4), k1 = kd + s2 * (kStepBytes >> 4), v1 = vd + s2 * (kStepBytes >> 4);
+        const uint64_t k0 = kd + s * (kKeyBytes >> 4), k1 = kd + s2 * (kKeyBytes >> 4), v1 = vd + s2 * (kKeyBytes >> 4);
         if (more) {
-          if (!wait_all(&sm.s_read[g], m & 1, abort, st) || !loaded(j + 2)) break;
+          if (!wait_all(&sm.s_read[g], m & 1, abort, st) || !loaded(j + G)) break;
           tc_fence_after();
           if (elect_one()) {
-            mma_rows(buf, qd, k1);
+            mma_rows<kKeyStep>(buf, qd, k1, false);
             umma_commit(&sm.s_full[g]);
           }
           __syncwarp();
@@ -694,10 +712,10 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
         if (!wait_all(&sm.ds_ready[g], m & 1, abort, st)) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_cols(acc, buf + kStep, k0, m > 0);
+          mma_cols<kKeyStep>(acc, buf + kKeyStep, k0, m > 0);
           umma_commit(&sm.kv_empty[s]);
           if (more) {
-            mma_rows(buf + kStep, gd, v1);                      // over the dS that dQ reads
+            mma_rows<kKeyStep>(buf + kKeyStep, gd, v1, false);  // over the dS that dQ reads
             umma_commit(&sm.dp_full[g]);
           }
         }
@@ -708,51 +726,51 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
         drain_mma(&sm.drain, 0);
       }
       __syncwarp();
-    } else if (warp == 2 && n > 0 && n_last < kStep) {
+    } else if (warp == 2 && n > 0 && n_last < kKeyStep) {
       // ------------------------------------------------------------ K rows behind the union of the ranges
       const int s = (n - 1) % kKvStages;
       if (__all_sync(0xffffffffu, mbar_wait(&sm.dirty, 0, abort, st)) &&
           __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[s], ((n - 1) / kKvStages) & 1, abort, st))) {
-        zero_rows(sm.k[s], kStep, [&](int r) { return r >= n_last; });
+        zero_rows(sm.k[s], kKeyStep, [&](int r) { return r >= n_last; });
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.clean);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegs) : "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWorkRegs) : "memory");
     // ------------------------------------------------------------ dS
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lane_off + grp * 2 * kStep + half * kCols, td = ts + kStep;
+    const uint32_t ts = tmem + lane_off + grp * 2 * kKeyStep + half * kKeyCols, td = ts + kKeyStep;
     const float m2 = l < a.L ? nlse[(size_t)bh * Lp + l] : -INFINITY, nd = l < a.L ? ndsum[(size_t)bh * Lp + l] : 0.f;
-    const int c0 = base + half * kCols;                         // the key of this thread's first column in step 0
+    const int c0 = base + half * kKeyCols;                         // the key of this thread's first column in step 0
     const int f_lo = warp_max(live ? keys.x : 0) - c0;          // every live row of the warp sees [f_lo, f_hi)
     const int f_hi = warp_min(live ? keys.y : 0x7fffffff) - c0;
     const unsigned long long cc = f2_pack(a.scale_log2, a.scale_log2), mm = f2_pack(m2, m2), dd = f2_pack(nd, nd);
     bool ok = true;
-    for (int j = grp; j < n; j += 2) {
-      const int m = j >> 1;
+    for (int j = grp; j < n; j += G) {
+      const int m = j / G;
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[grp], m & 1, abort, st))) { ok = false; break; }
       tc_fence_after();
-      uint32_t p[kCols];
+      uint32_t p[kKeyCols];
 #pragma unroll
-      for (int c = 0; c < kCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
+      for (int c = 0; c < kKeyCols; c += kChunk) tmem_ld16(ts + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&sm.s_read[grp]);
-      const bool masked = f_lo > j * kStep || f_hi < j * kStep + kCols;
+      const bool masked = f_lo > j * kKeyStep || f_hi < j * kKeyStep + kKeyCols;
 #pragma unroll
-      for (int e = 0; e < kCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc, mm);
+      for (int e = 0; e < kKeyCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc, mm);
       if (masked) {
-        const int first = keys.x - c0 - j * kStep, last = keys.y - c0 - j * kStep;
+        const int first = keys.x - c0 - j * kKeyStep, last = keys.y - c0 - j * kKeyStep;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e)
+        for (int e = 0; e < kKeyCols; ++e)
           if (e < first || e >= last) p[e] = 0u;
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.dp_full[grp], m & 1, abort, st))) { ok = false; break; }
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < kCols; c += kChunk) {
+      for (int c = 0; c < kKeyCols; c += kChunk) {
         uint32_t g[16], pk[8];
         tmem_ld16(td + c, g);
         tmem_wait_ld();
@@ -772,22 +790,19 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.drain, 0, abort, st));
     tc_fence_after();
     if (ok) {
-      // each of the 2 kHalves warpgroups stores its channels
-      constexpr int kOut = kAttnD / (2 * kHalves);
-      const int o0 = (grp * kHalves + half) * kOut;
+      constexpr int kOut = kAttnD / (2 * G);                    // channels of a warpgroup
+      const int o0 = wg * kOut;
       uint32_t o[kOut];
-      if (n > 0) {
+      auto sum_of = [&](int g, uint32_t (&x)[kOut]) {
 #pragma unroll
         for (int c = 0; c < kOut; c += 16)
-          tmem_ld16(tmem + lane_off + kColA + o0 + c, *reinterpret_cast<uint32_t(*)[16]>(&o[c]));
+          tmem_ld16(tmem + lane_off + C::kColQ + g * kAttnD + o0 + c, *reinterpret_cast<uint32_t(*)[16]>(&x[c]));
         tmem_wait_ld();
-      }
-      if (n > 1) {                                              // the second group's sum
+      };
+      if (n > 0) sum_of(0, o);
+      if (G == 2 && n > 1) {                                    // the second group's sum
         uint32_t x[kOut];
-#pragma unroll
-        for (int c = 0; c < kOut; c += 16)
-          tmem_ld16(tmem + lane_off + kColB + o0 + c, *reinterpret_cast<uint32_t(*)[16]>(&x[c]));
-        tmem_wait_ld();
+        sum_of(1, x);
 #pragma unroll
         for (int e = 0; e < kOut; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(x[e]));
       }
@@ -809,7 +824,7 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
     if (*abort)
       for (int i = 0; i < 200; ++i) __nanosleep(1000);           // copies in flight land
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -817,20 +832,31 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
+// Groups a block.  Two blocks of one group hide each other's start and end
+// (about 7 us a block: setting up, the first loads and products, the drain);
+// one block of two groups has longer steps and is faster once it has enough
+// of them.  dK/dV at 16 heads: 8 x 1,369 tokens 170 us with two blocks, 178
+// with one; 4 x 2,738 288 and 274; 8,214 593 and 515; 64 x 128 40 and 61.  dQ:
+// 137 and 154; 223 and 228; 473 and 415; 37 and 54.
+//
 // Splits of a key tile's queries: as for the forward, waves of CTAs times
 // their steps plus about three steps of start and end.
 AttnBwdPlan attn_bwd_plan(const httm_attention& a) {
   AttnBwdPlan p{};
-  p.q_tiles = (a.q_len + kStep - 1) / kStep;
+  const long long group = a.heads / a.kv_heads;
+  p.kv_groups = group * a.q_len <= 16 * kAttnTile ? 1 : 2;
+  p.q_groups = a.kv_len <= 22 * kAttnTile ? 1 : 2;
+  p.step = p.kv_groups == 1 ? Cfg<1>::kStep : Cfg<2>::kStep;
+  p.q_tiles = (a.q_len + p.step - 1) / p.step;
   p.k_tiles = (a.kv_len + kAttnTile - 1) / kAttnTile;
-  p.Lp = p.q_tiles * kStep;
+  p.Lp = p.q_tiles * p.step;
   const long long items = (long long)a.batch * a.kv_heads * p.k_tiles;
-  const long long steps = (long long)(a.heads / a.kv_heads) * p.q_tiles;
+  const long long steps = group * p.q_tiles, slots = kSMs * (3 - p.kv_groups);
   p.kv_parts = 1;
   double best = 0;
   for (int n = 1; n <= std::min<long long>(16, std::max<long long>(1, steps)) && items > 0; ++n) {
-    if (n > 1 && items * n > 4 * kSMs) break;
-    const long long waves = (items * n + kSMs - 1) / kSMs;
+    if (n > 1 && items * n > 4 * slots) break;
+    const long long waves = (items * n + slots - 1) / slots;
     const double cost = (double)waves * ((steps + n - 1) / n + 3) + (n > 1 ? 4 + n / 4.0 : 0);
     if (n == 1 || cost < best) best = cost, p.kv_parts = n;
   }
@@ -849,47 +875,74 @@ AttnBwdPlan attn_bwd_plan(const httm_attention& a) {
   return p;
 }
 
+namespace {
+
+struct BwdBuffers {
+  float *nlse, *ndsum, *part;
+  uint4* extra;
+  int2* ranges;
+  AttnTileRange* tiles;
+};
+
+// With no queries (or no keys) nothing is loaded through their maps.
+bool bwd_maps(const AttnArgs& a, int q_box, int kv_box, AttnMap (&m)[4]) {
+  const void* any = a.L > 0 ? a.q.data : a.k.data;
+  return attn_map(&m[0], a.q, any, a.d, a.L, a.H, a.B, q_box) && attn_map(&m[1], a.dout, any, a.d, a.L, a.H, a.B, q_box) &&
+         attn_map(&m[2], a.k, any, a.d, a.N, a.K, a.B, kv_box) && attn_map(&m[3], a.v, any, a.d, a.N, a.K, a.B, kv_box);
+}
+
+template <int G>
+cudaError_t launch_dkv(const AttnArgs& a, const AttnBwdPlan& p, const BwdBuffers& w, cudaStream_t s) {
+  using C = Cfg<G>;
+  cudaError_t e;
+  if (p.q_tiles > 0) {
+    attn_prep_kernel<C::kStep><<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, w.nlse, w.ndsum, w.extra,
+                                                                         w.ranges, w.tiles);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (p.k_tiles == 0) return cudaSuccess;
+  AttnMap m[4];
+  if (!bwd_maps(a, C::kStep, kAttnTile, m)) return cudaErrorInvalidValue;
+  e = cudaFuncSetAttribute(attn_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDkvSmem<G>);
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)a.B * a.K * p.k_tiles;
+  attn_dkv_kernel<G><<<(unsigned)(items * p.kv_parts), C::kThreads, kDkvSmem<G>, s>>>(
+      m[0], m[1], m[2], m[3], a, p.q_tiles, p.k_tiles, p.kv_parts, w.extra, w.ranges, w.tiles, w.part);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.kv_parts == 1) return e;
+  const long long rows = 2ll * a.B * a.K * a.N;
+  attn_dkv_join_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, s>>>(a, p.k_tiles, p.kv_parts, w.part);
+  return cudaGetLastError();
+}
+
+template <int G>
+cudaError_t launch_dq(const AttnArgs& a, const AttnBwdPlan& p, const BwdBuffers& w, cudaStream_t s) {
+  using C = Cfg<G>;
+  if (a.L == 0) return cudaSuccess;
+  AttnMap m[4];
+  if (!bwd_maps(a, kAttnTile, C::kKeyStep, m)) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem<G>);
+  if (e != cudaSuccess) return e;
+  const long long m_tiles = (a.L + kAttnTile - 1) / kAttnTile;
+  attn_dq_kernel<G><<<(unsigned)(a.B * a.H * m_tiles), C::kThreads, kDqSmem<G>, s>>>(m[0], m[1], m[2], m[3], a, p.Lp,
+                                                                                   w.nlse, w.ndsum, w.ranges);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnBwdPlan& p, void* ws, cudaStream_t s) {
   char* w = static_cast<char*>(ws);
-  float* nlse = reinterpret_cast<float*>(w + p.stat);
-  float* ndsum = nlse + (size_t)a.B * a.H * p.Lp;
-  uint4* extra = reinterpret_cast<uint4*>(w + p.extra);
-  int2* ranges = reinterpret_cast<int2*>(w + p.range);
-  AttnTileRange* tiles = reinterpret_cast<AttnTileRange*>(w + p.tiles);
-  float* part = reinterpret_cast<float*>(w + p.part);
-  AttnMap mq, mg, mk, mv;
-  // with no queries (or no keys) nothing is loaded through their maps
-  const void* any = a.L > 0 ? a.q.data : a.k.data;
-  auto maps = [&](int q_box, int kv_box) {
-    return attn_map(&mq, a.q, any, a.d, a.L, a.H, a.B, q_box) && attn_map(&mg, a.dout, any, a.d, a.L, a.H, a.B, q_box) &&
-           attn_map(&mk, a.k, any, a.d, a.N, a.K, a.B, kv_box) && attn_map(&mv, a.v, any, a.d, a.N, a.K, a.B, kv_box);
-  };
-  if (!maps(kStep, kAttnTile)) return cudaErrorInvalidValue;
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDkvSmem)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem)) != cudaSuccess)
-    return e;
-  if (p.q_tiles > 0) {
-    attn_prep_kernel<<<dim3(p.q_tiles, a.B * a.H), 256, 0, s>>>(a, p.q_tiles, nlse, ndsum, extra, ranges, tiles);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  if (p.k_tiles > 0) {
-    const long long items = (long long)a.B * a.K * p.k_tiles;
-    attn_dkv_kernel<<<(unsigned)(items * p.kv_parts), kThreads, kDkvSmem, s>>>(
-        mq, mg, mk, mv, a, p.q_tiles, p.k_tiles, p.kv_parts, extra, ranges, tiles, part);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.kv_parts > 1) {
-      const long long rows = 2ll * a.B * a.K * a.N;
-      attn_dkv_join_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, s>>>(a, p.k_tiles, p.kv_parts, part);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-  }
-  if (!maps(kAttnTile, kStep)) return cudaErrorInvalidValue;
-  const long long m_tiles = (a.L + kAttnTile - 1) / kAttnTile;
-  if (m_tiles > 0)
-    attn_dq_kernel<<<(unsigned)(a.B * a.H * m_tiles), kThreads, kDqSmem, s>>>(mq, mg, mk, mv, a, p.q_tiles,
-                                                                                         nlse, ndsum, ranges);
-  return cudaGetLastError();
+  BwdBuffers buf;
+  buf.nlse = reinterpret_cast<float*>(w + p.stat);
+  buf.ndsum = buf.nlse + (size_t)a.B * a.H * p.Lp;
+  buf.extra = reinterpret_cast<uint4*>(w + p.extra);
+  buf.ranges = reinterpret_cast<int2*>(w + p.range);
+  buf.tiles = reinterpret_cast<AttnTileRange*>(w + p.tiles);
+  buf.part = reinterpret_cast<float*>(w + p.part);
+  const cudaError_t e = p.kv_groups == 1 ? launch_dkv<1>(a, p, buf, s) : launch_dkv<2>(a, p, buf, s);
+  if (e != cudaSuccess) return e;
+  return p.q_groups == 1 ? launch_dq<1>(a, p, buf, s) : launch_dq<2>(a, p, buf, s);
 }
 
 }  // namespace httm
