@@ -148,6 +148,9 @@ def test_against_definition(case):
 def test_without_parameters_or_stream_gradient():
     _compare(33, 96, BF, BF, RMS, LAYER, 1, weight=False, bias=False)
     _compare(33, 96, F32, BF, NONE, RMS, 0, bias=False, with_dy=False)
+    # nothing multiplies the threads behind the row's end by a weight of 0
+    for C in (2, 24, 150, 315, 1030, 5000):
+        _compare(9, C, F32, F32, LAYER, LAYER, 0, weight=False, bias=False)
 
 
 def test_norm_before_a_first_block():

@@ -379,7 +379,8 @@ gated_norm_grad_kernel(NormArgs a) {
       row_sums<NT, 2>(s, tmp, turn);
       const float m0 = a.pre == HTTM_NORM_LAYER ? s[0] * inv_c : 0.f, m1 = s[1] * inv_c;
 #pragma unroll
-      for (int e = 0; e < E; ++e) g[e] = fmaf(r_pre, dz[e] - m0 - y[e] * m1, g[e]);
+      for (int e = 0; e < E; ++e)                             // (behind the row's end: 0, not -m0)
+        g[e] = cols.live(0, e) ? fmaf(r_pre, dz[e] - m0 - y[e] * m1, g[e]) : 0.f;
     }
     if (a.dx) {
       float o[E];
