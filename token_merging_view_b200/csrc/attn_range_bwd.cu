@@ -16,7 +16,7 @@
 //    from shared memory would cost 8 bytes an element of its bandwidth, as
 //    much as all else together (dK/dV 1087 us).  Instead one more K step of
 //    each product adds them: a row of ones times -lse / scale (-D) as the sum
-//    of three bf16, which holds an fp32 whole (XXX us);
+//    of three bf16, which holds an fp32 whole (1023 us);
 //  - attn_dq_kernel: a CTA owns 128 queries and walks over their keys; dS is
 //    the A operand of dQ += dS K.
 // Seven products a tile where one fused pass has five: dQ gathered from
@@ -59,7 +59,8 @@ struct Cfg {
   // registers a thread: launched at 80 or 96, then 128 kAuxRegs + 256 G
   // kWorkRegs of the same total
   static constexpr int kLaunchRegs = G == 1 ? 80 : 96, kAuxRegs = G == 1 ? 48 : 64, kWorkRegs = G == 1 ? 96 : 104;
-  static_assert(128 * kAuxRegs + 256 * G * kWorkRegs <= kThreads * kLaunchRegs, "registers");
+  static constexpr int kRegs = 128 * kAuxRegs + 256 * G * kWorkRegs;
+  static_assert(kRegs <= kThreads * kLaunchRegs, "registers");
   static_assert(kBlocks * kThreads * kLaunchRegs <= 65536, "registers");
   // dK, dV: queries of a step, columns of a thread, query tiles in flight
   static constexpr int kStep = G == 1 ? 64 : 96, kCols = kStep / 2, kStages = G == 1 ? 3 : 5;
@@ -903,6 +904,8 @@ cudaError_t launch_dkv(const AttnArgs& a, const AttnBwdPlan& p, const BwdBuffers
   if (p.k_tiles == 0) return cudaSuccess;
   AttnMap m[4];
   if (!bwd_maps(a, C::kStep, kAttnTile, m)) return cudaErrorInvalidValue;
+  static const cudaError_t regs = check_registers(attn_dkv_kernel<G>, C::kThreads, C::kRegs);
+  if (regs != cudaSuccess) return regs;
   e = cudaFuncSetAttribute(attn_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDkvSmem<G>);
   if (e != cudaSuccess) return e;
   const long long items = (long long)a.B * a.K * p.k_tiles;
@@ -920,6 +923,8 @@ cudaError_t launch_dq(const AttnArgs& a, const AttnBwdPlan& p, const BwdBuffers&
   if (a.L == 0) return cudaSuccess;
   AttnMap m[4];
   if (!bwd_maps(a, kAttnTile, C::kKeyStep, m)) return cudaErrorInvalidValue;
+  static const cudaError_t regs = check_registers(attn_dq_kernel<G>, C::kThreads, C::kRegs);
+  if (regs != cudaSuccess) return regs;
   const cudaError_t e =
       cudaFuncSetAttribute(attn_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem<G>);
   if (e != cudaSuccess) return e;

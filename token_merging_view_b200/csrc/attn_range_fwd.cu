@@ -43,6 +43,7 @@ using namespace tc;
 
 constexpr int kStages = 4;
 constexpr int kThreads = 384;
+constexpr int kAuxRegs = 88, kSoftmaxRegs = 208;   // of 384 x 168 at launch
 constexpr uint32_t kColO = 384;           // O_t at kColO + 64 t; S ring at 0, 128, 256
 constexpr int kPartStride = httm::kAttnRangePart;
 
@@ -151,7 +152,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
   const int n_last = hi - (base + (n_kv - 1) * kAttnTile);   // keys of the union in the last tile
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs) : "memory");
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------ producer
       for (int j = 0; j < n_kv; ++j) {
@@ -225,7 +226,7 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs) : "memory");
     // -------------------------------------------------------------- softmax
     if (t < n_t) {
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -518,6 +519,9 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, c
   if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B, kAttnTile) ||
       !attn_map(&mv, a.v, a.q.data, a.d, a.N, a.K, a.B, kAttnTile))
     return cudaErrorInvalidValue;
+  static const cudaError_t regs =
+      check_registers(attn_range_fwd_kernel, kThreads, 128 * kAuxRegs + 256 * kSoftmaxRegs);
+  if (regs != cudaSuccess) return regs;
   cudaError_t e =
       cudaFuncSetAttribute(attn_range_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;

@@ -56,6 +56,17 @@ inline bool disjoint(const View& v, int64_t batch, int64_t heads, int64_t tokens
   return true;
 }
 
+// A kernel whose warps exchange registers (setmaxnreg) waits forever if it
+// was launched with fewer than it hands out: checked once against what the
+// compiler gave it.
+template <class K>
+inline cudaError_t check_registers(K* kernel, int threads, int total) {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  if (e != cudaSuccess) return e;
+  return at.numRegs * threads >= total ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 #define HTTM_OPS_LAUNCH(expr, s)                              \
   do {                                                        \
     const cudaError_t e_ = ::httm::checked((expr), (s));      \
