@@ -116,6 +116,16 @@ def test_against_definition(case):
     _compare(q, k, v, dout, b, e)
 
 
+@pytest.mark.parametrize("case", [(37, 4, 4, 129, 8300, 64, "padded"), (37, 4, 2, 257, 8193, 24, "random"),
+                                  (37, 4, 4, 129, 8192, 64, "random"), (37, 4, 4, 100, 97, 64, "padded"),
+                                  (9, 4, 2, 700, 96, 64, "none"), (9, 4, 1, 301, 193, 40, "window")],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_more_items_than_sms(case):
+    """Enough rows that no keys are split: more than 8,192 keys and fewer, and
+    steps of the keys that end at, before and behind a tile."""
+    test_against_definition(case)
+
+
 def test_scale_and_large_scores():
     """Scores far apart: the running maximum rises by more than 2^16 between
     tiles, and some probabilities underflow to 0."""
@@ -230,7 +240,8 @@ def test_visible_nan_reaches_its_row():
 
 
 @pytest.mark.parametrize("G,L,N,mask", [(1, 300, 300, "causal"), (2, 300, 700, "random"), (1, 7, 90, "causal"),
-                                        (4, 6, 1000, "random"), (1, 600, 5000, "window"), (1, 9, 20000, "random")])
+                                        (4, 6, 1000, "random"), (1, 600, 5000, "window"), (1, 9, 20000, "random"),
+                                        (1, 18900, 8300, "random")])
 def test_values_reach_only_the_rows_that_see_them(G, L, N, mask):
     """Infinities and NaN in values (and NaN in keys) that some rows see and
     some do not: the others keep their bits, and those that see an infinity in

@@ -33,14 +33,14 @@ struct AttnMap {
 };
 bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, int heads, int batch, int box);
 
-// Forward: work items of up to 256 query rows, each in `parts` key ranges.
+// Forward: work items of up to tile_rows query rows, each in `parts` key ranges.
 // With at most kAttnFewRows rows a key head the kernel for few rows runs.
 constexpr int kAttnFewRows = 32;
 constexpr int kAttnCluster = 8;         // parts of few rows that are added up inside one launch
 constexpr int kAttnRangePart = 68;     // floats of a partial row: O (64), sum, maximum (log2), 2 unused
 struct AttnFwdPlan {
-  bool few;
-  int rows, row_tiles, parts;           // rows = L * G of one key head
+  bool few, pair;                       // the kernel: for few rows, two blocks an SM, else one
+  int rows, tile_rows, row_tiles, parts;   // rows = L * G of one key head
   long long items;                      // B * K * row_tiles
   size_t part_bytes;
 };
