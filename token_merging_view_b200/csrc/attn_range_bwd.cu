@@ -904,8 +904,8 @@ cudaError_t launch_dkv(const AttnArgs& a, const AttnBwdPlan& p, const BwdBuffers
   if (p.k_tiles == 0) return cudaSuccess;
   AttnMap m[4];
   if (!bwd_maps(a, C::kStep, kAttnTile, m)) return cudaErrorInvalidValue;
-  static const cudaError_t regs = check_registers(attn_dkv_kernel<G>, C::kThreads, C::kRegs);
-  if (regs != cudaSuccess) return regs;
+  e = check_registers<attn_dkv_kernel<G>>(C::kThreads, C::kRegs);
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attn_dkv_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDkvSmem<G>);
   if (e != cudaSuccess) return e;
   const long long items = (long long)a.B * a.K * p.k_tiles;
@@ -923,10 +923,9 @@ cudaError_t launch_dq(const AttnArgs& a, const AttnBwdPlan& p, const BwdBuffers&
   if (a.L == 0) return cudaSuccess;
   AttnMap m[4];
   if (!bwd_maps(a, kAttnTile, C::kKeyStep, m)) return cudaErrorInvalidValue;
-  static const cudaError_t regs = check_registers(attn_dq_kernel<G>, C::kThreads, C::kRegs);
-  if (regs != cudaSuccess) return regs;
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem<G>);
+  cudaError_t e = check_registers<attn_dq_kernel<G>>(C::kThreads, C::kRegs);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attn_dq_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDqSmem<G>);
   if (e != cudaSuccess) return e;
   const long long m_tiles = (a.L + kAttnTile - 1) / kAttnTile;
   attn_dq_kernel<G><<<(unsigned)(a.B * a.H * m_tiles), C::kThreads, kDqSmem<G>, s>>>(m[0], m[1], m[2], m[3], a, p.Lp,

@@ -850,22 +850,18 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, c
   if (!attn_map(&mk, a.k, a.q.data, a.d, a.N, a.K, a.B, keys) || !attn_map(&mv, a.v, a.q.data, a.d, a.N, a.K, a.B, keys))
     return cudaErrorInvalidValue;
   if (p.pair) {
-    static const cudaError_t regs =
-        check_registers(attn_range_pair_kernel, kPairThreads, 128 * kPairAux + 128 * kPairSoft);
-    if (regs != cudaSuccess) return regs;
-    cudaError_t e =
-        cudaFuncSetAttribute(attn_range_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    cudaError_t e = check_registers<attn_range_pair_kernel>(kPairThreads, 128 * kPairAux + 128 * kPairSoft);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_range_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
     if (e != cudaSuccess) return e;
     attn_range_pair_kernel<<<(unsigned)(p.items * p.parts), kPairThreads, kPairSmem, s>>>(mk, mv, a, p.row_tiles,
                                                                                          p.parts, part);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join(a, p, part, s);
   }
-  static const cudaError_t regs =
-      check_registers(attn_range_fwd_kernel, kThreads, 128 * kAuxRegs + 256 * kSoftmaxRegs);
-  if (regs != cudaSuccess) return regs;
-  cudaError_t e =
-      cudaFuncSetAttribute(attn_range_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  cudaError_t e = check_registers<attn_range_fwd_kernel>(kThreads, 128 * kAuxRegs + 256 * kSoftmaxRegs);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attn_range_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   attn_range_fwd_kernel<<<(unsigned)(p.items * p.parts), kThreads, kSmemBytes, s>>>(mk, mv, a, p.row_tiles, p.parts,
                                                                                     part);

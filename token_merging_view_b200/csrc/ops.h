@@ -4,6 +4,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/httm.h"
 #include "internal.h"
 
@@ -57,14 +59,18 @@ inline bool disjoint(const View& v, int64_t batch, int64_t heads, int64_t tokens
 }
 
 // A kernel whose warps exchange registers (setmaxnreg) waits forever if it
-// was launched with fewer than it hands out: checked once against what the
-// compiler gave it.
-template <class K>
-inline cudaError_t check_registers(K* kernel, int threads, int total) {
+// was launched with fewer than it hands out: checked against what the
+// compiler gave it, until that once succeeded.
+template <auto kKernel>
+inline cudaError_t check_registers(int threads, int total) {
+  static std::atomic<bool> enough{false};
+  if (enough.load(std::memory_order_relaxed)) return cudaSuccess;
   cudaFuncAttributes at;
-  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  const cudaError_t e = cudaFuncGetAttributes(&at, kKernel);
   if (e != cudaSuccess) return e;
-  return at.numRegs * threads >= total ? cudaSuccess : cudaErrorInvalidConfiguration;
+  if (at.numRegs * threads < total) return cudaErrorInvalidConfiguration;
+  enough.store(true, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 #define HTTM_OPS_LAUNCH(expr, s)                              \
