@@ -11,8 +11,10 @@
 // taken before the squares, so the variance does not cancel.
 //
 // Threads: a row belongs to NT threads, each with V vectors of 8 channels.
-// Forward uses one warp a row up to 512 channels and two up to 1,024 (67.6 us
-// at 41,070 x 1,024 bf16, one warp a row 73, four 85).
+// Forward uses one warp a row up to 512 channels and two up to 1,024 (65 us
+// at 41,070 x 1,024 bf16, one warp a row 72, four 81); rows that only single
+// elements can be taken from have twice the threads (5,476 x 1,001 fp32
+// stream: 17 us against 20).
 // Backward keeps the sums of up to five parameter gradients in registers
 // while a thread group walks over its rows, so it spreads a row over more
 // threads; each group writes one row of partial sums, which a second kernel
@@ -157,22 +159,51 @@ struct Raw {
   }
 };
 
-// Sum over the NT threads of a row (all of them get it).  NT = 32: shuffles;
-// more: one row per block, through `tmp` (2 x 32 floats, used in turn so one
-// barrier per sum is enough).
+// K sums (1 or 2) over the NT threads of a row; all of them get them.  Two
+// share a warp's shuffles: the first exchange leaves one sum's terms to each
+// half of the warp.  NT > 32 is one row a block: the warps' sums meet in
+// `tmp` (used in turn, so one barrier is enough), where every thread adds
+// them up itself, four a load, instead of by shuffles again (the gradients
+// of 41,070 x 1,024 bf16: 121 -> 118 us).
+template <int K>
+using RowTmp = float[2][K][32];
 template <int NT, int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float (*tmp)[K][32], int& turn) {
+__device__ __forceinline__ void row_sums(float (&v)[K], RowTmp<K>& tmp, int& turn) {
+  static_assert(K == 1 || K == 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool upper = lane & 16;
+  float x = v[0];
+  if constexpr (K == 2) {
+    x = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
+  } else {
+    x += __shfl_xor_sync(0xffffffffu, x, 16);
+  }
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if constexpr (NT > 32) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) tmp[turn][k][warp] = v[k];
+  for (int h = 8; h > 0; h >>= 1) x += __shfl_xor_sync(0xffffffffu, x, h);
+  if constexpr (NT == 32) {
+    v[0] = x;
+    if constexpr (K == 2) {
+      const float o = __shfl_xor_sync(0xffffffffu, x, 16);
+      v[0] = upper ? o : x;
+      v[1] = upper ? x : o;
     }
+  } else {
+    if (K == 2 ? (lane & 15) == 0 : lane == 0) tmp[turn][K == 2 ? lane >> 4 : 0][warp] = x;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < NT / 32 ? tmp[turn][k][lane] : 0.f);
+    for (int k = 0; k < K; ++k) {
+      const float* t = tmp[turn][k];
+      if constexpr (NT == 64) {
+        v[k] = t[0] + t[1];
+      } else {
+        v[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT / 128; ++i) {
+          const float4 q = reinterpret_cast<const float4*>(t)[i];
+          v[k] += (q.x + q.y) + (q.z + q.w);
+        }
+      }
+    }
     turn ^= 1;
   }
 }
@@ -180,7 +211,7 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*tmp)[K][32], int
 // n = (v - mean) * r in place; returns mean and r.
 template <int NT, int W, int V>
 __device__ __forceinline__ void normalise(float (&v)[V][8], const Cols<NT, W>& cols, int kind, float eps, float inv_c,
-                                          float (*tmp)[1][32], int& turn, float& mean, float& r) {
+                                          RowTmp<1>& tmp, int& turn, float& mean, float& r) {
   mean = 0.f;
   float s[1];
   if (kind == HTTM_NORM_LAYER) {
@@ -229,7 +260,7 @@ __device__ __forceinline__ void affine(float (&v)[V][8], const Cols<NT, W>& cols
 template <class TX, class TF, int NT, int V, int W>
 __global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs a) {
   constexpr int kRows = NT > 32 ? 1 : 4;                      // rows per block (barriers need one)
-  __shared__ float tmp[2][1][32];
+  __shared__ __align__(16) RowTmp<1> tmp;
   int turn = 0;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
   if (row >= a.rows) return;                                  // whole warps: NT is a multiple of 32
@@ -285,26 +316,32 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 128) gated_norm_kernel(NormArgs
   }
 }
 
-// Backward: channels a thread, threads a row, and the blocks an SM is to
-// hold.  With 4 channels the sums and the row in flight fit 80 registers (24
-// warps an SM); rows of over 4,096 channels take 8.
-constexpr int grad_channels(int C) { return C <= 4096 ? 4 : 8; }
-constexpr int grad_threads(int C) {
+// Backward: channels a thread, threads a row and blocks an SM.  The parameter
+// sums and the row in flight are the registers: 8 channels a thread, or with
+// five sums up to 2,048 channels 4, fit the 128 of 512 threads an SM (20,000
+// rows, 8 against 4 channels: 1,024 bf16 47 and 52 us, 256 33 and 38, 2,048
+// fp32 72 and 117; with five sums 1,024 fp32 134 and 82, 4,096 bf16 90 and
+// 174).  More threads with fewer registers are no faster: 4 channels, five
+// sums, 1,024 fp32 at 512 / 768 / 1,024 threads 82 / 107 / 140.  At over
+// 4,096 channels a row takes 1,024 threads, and registers spill: 8,192 bf16
+// 104 us, with five sums 186.
+constexpr int grad_channels(int C, bool post) { return post && C <= 2048 ? 4 : 8; }
+constexpr int grad_threads(int C, int E) {
   int nt = 32;
-  while (nt * grad_channels(C) < C) nt *= 2;
+  while (nt * E < C) nt *= 2;
   return nt;
 }
-constexpr int grad_blocks(int NT, int E) { return E == 8 || NT == 1024 ? 1 : 768 / (NT > 32 ? NT : 128); }
+constexpr int grad_blocks(int NT) { return NT == 1024 ? 1 : 512 / (NT > 32 ? NT : 128); }
 
 // Backward: thread group g of gate group q walks over its share of that
 // group's rows with E channels a thread, one row ahead with its loads.  POST:
 // there is a norm on the block's output (two more parameter gradients and
 // another pair of sums a row).
 template <class TX, class TF, int NT, int W, bool POST, int E>
-__global__ void __launch_bounds__(NT > 32 ? NT : 128, grad_blocks(NT, E))
+__global__ void __launch_bounds__(NT > 32 ? NT : 128, grad_blocks(NT))
 gated_norm_grad_kernel(NormArgs a) {
   constexpr int kGroups = NT > 32 ? 1 : 4;                    // thread groups per block (barriers need one)
-  __shared__ float tmp[2][2][32];
+  __shared__ __align__(16) RowTmp<2> tmp;
   int turn = 0;
   const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / NT;
   const int n_gates = max(1, a.gates);
@@ -471,9 +508,8 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
 // hold at once, at least 4 rows a group.
 int grad_chunks(const httm_norm_cfg& c) {
   const int64_t gates = std::max(1, c.gates), rows = c.rows / gates;
-  const int nt = grad_threads(c.channels);
-  const int64_t per_sm = grad_blocks(nt, grad_channels(c.channels)) * (nt > 32 ? 1 : 4);
-  const int64_t want = std::max<int64_t>(1, kSMs * per_sm / gates);
+  const int nt = grad_threads(c.channels, grad_channels(c.channels, c.post != HTTM_NORM_NONE));
+  const int64_t want = std::max<int64_t>(1, kSMs * grad_blocks(nt) * (nt > 32 ? 1 : 4) / gates);
   return (int)std::max<int64_t>(1, std::min(want, rows / 4));
 }
 
@@ -485,7 +521,12 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
     const int64_t grid = (a.rows + kRows - 1) / kRows;                                              \
     gated_norm_kernel<TX, TF, NT, V, W><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a);     \
   } while (0)
-  if (a.C <= 256) HTTM_NORM_FWD(32, 1);
+  if (W == 1 && a.C > 512) {
+    if (a.C <= 1024) HTTM_NORM_FWD(128, 1);
+    else if (a.C <= 2048) HTTM_NORM_FWD(256, 1);
+    else if (a.C <= 4096) HTTM_NORM_FWD(512, 1);
+    else HTTM_NORM_FWD(1024, 1);
+  } else if (a.C <= 256) HTTM_NORM_FWD(32, 1);
   else if (a.C <= 512) HTTM_NORM_FWD(32, 2);
   else if (a.C <= 1024) HTTM_NORM_FWD(64, 2);
   else if (a.C <= 2048) HTTM_NORM_FWD(128, 2);
@@ -503,14 +544,16 @@ cudaError_t launch_grad(const NormArgs& a, cudaStream_t s) {
     const int64_t grid = ((int64_t)std::max(1, a.gates) * a.chunks + kGroups - 1) / kGroups;          \
     gated_norm_grad_kernel<TX, TF, NT, (W < E ? W : E), POST, E><<<(unsigned)grid, (NT) > 32 ? (NT) : 128, 0, s>>>(a); \
   } while (0)
-  if (grad_channels(a.C) == 8) HTTM_NORM_BWD(1024, 8);
-  else switch (grad_threads(a.C)) {
-    case 32: HTTM_NORM_BWD(32, 4); break;
-    case 64: HTTM_NORM_BWD(64, 4); break;
-    case 128: HTTM_NORM_BWD(128, 4); break;
-    case 256: HTTM_NORM_BWD(256, 4); break;
-    case 512: HTTM_NORM_BWD(512, 4); break;
-    default: HTTM_NORM_BWD(1024, 4); break;
+  constexpr int E = POST ? 4 : 8;
+  switch (grad_channels(a.C, POST) == E ? grad_threads(a.C, E) : 0) {
+    case 32: HTTM_NORM_BWD(32, E); break;
+    case 64: HTTM_NORM_BWD(64, E); break;
+    case 128: HTTM_NORM_BWD(128, E); break;
+    case 256: HTTM_NORM_BWD(256, E); break;
+    case 512: HTTM_NORM_BWD(512, E); break;
+    default:
+      if (a.C <= 4096) HTTM_NORM_BWD(512, 8);
+      else HTTM_NORM_BWD(1024, 8);
   }
 #undef HTTM_NORM_BWD
   return cudaGetLastError();
