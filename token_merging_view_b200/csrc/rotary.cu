@@ -101,7 +101,7 @@ __device__ __forceinline__ void turn_pair(float a, float b, float c, float s, fl
 }
 
 // heads read ahead: 185 us without, 139 with 4, 130 with 8 (41,070 tokens x 32
-// heads, twice); the element accesses of odd shapes are slower with 8
+// heads, twice, in one group); the element accesses of odd shapes are slower with 8
 template <int W>
 constexpr int kHeadsAhead = W == 8 ? 8 : 4;
 
@@ -205,6 +205,18 @@ cudaError_t launch_w(RotaryArgs& a, bool half, cudaStream_t s) {
   // threads an SM); with fewer tokens the heads are divided
   const long long want = (long long)kSMs * 1024;
   a.head_groups = (int)std::min<long long>(heads, std::max<long long>(1, (want + work - 1) / work));
+  if (W == 8 && a.head_groups == 1) {
+    // ... or as far as it fills the last wave of 512 threads an SM: a thread
+    // costs its batches of heads and 0.45 of one for its angles (41,070 tokens
+    // x 32 heads, twice, in 1 / 2 / 3 / 4 groups: 130 / 122 / 131 / 130 us)
+    double best = 0;
+    for (int g = 1; g <= std::min(heads, 4); ++g) {
+      const long long waves = (work * g + kSMs * 512 - 1) / (kSMs * 512);
+      const int per = (heads + g - 1) / g;
+      const double cost = (double)waves * ((per + kHeadsAhead<W> - 1) / kHeadsAhead<W> + 0.45);
+      if (g == 1 || cost < best) best = cost, a.head_groups = g;
+    }
+  }
   a.heads_per = (heads + a.head_groups - 1) / a.head_groups;
   a.head_groups = (heads + a.heads_per - 1) / a.heads_per;
   const int threads = work * a.head_groups < kSMs * 256 ? 64 : 256;
