@@ -145,6 +145,14 @@ def test_against_definition(case):
     _compare(*case)
 
 
+@pytest.mark.parametrize("post", [NONE, LAYER])
+@pytest.mark.parametrize("C", [256, 257, 512, 1032, 2048, 2049, 2050, 3016, 4096, 4097])
+def test_channels_a_thread(C, post):
+    """Both sides of every change in the threads a row takes, with more rows
+    than the GPU holds at a time and odd, paired and whole accesses."""
+    _compare(2500, C, BF, BF, post, LAYER, 2)
+
+
 def test_without_parameters_or_stream_gradient():
     _compare(33, 96, BF, BF, RMS, LAYER, 1, weight=False, bias=False)
     _compare(33, 96, F32, BF, NONE, RMS, 0, bias=False, with_dy=False)
