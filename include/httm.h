@@ -465,9 +465,11 @@ typedef struct {
  * result: a key or value no query of its batch entry attends to, and a
  * query, dout or out row whose range is empty, may hold anything (infinities
  * and NaN too).  A non-finite key or value that some queries attend to
- * reaches the outputs of those queries and no others.  In the gradients a
- * non-finite q, k, v or dout row that takes part may also reach rows of its
- * tiles (128 rows around it) that do not see it.
+ * reaches the outputs and the dq of those queries and no others (a score of
+ * -infinity is a probability of 0, which leaves both finite).  A non-finite
+ * query or dout row that takes part may also reach the dk and dv of keys it
+ * does not see: those that queries within 95 rows of it see, and what lies
+ * between these or within 127 keys of them.
  * Strides are multiples of 8 elements and data pointers 16-byte aligned
  * (else HTTM_ERR_ALIGN).  Inputs may be broadcast (stride 0 over batch or
  * heads; their gradients are then those of every copy, for the caller to

@@ -418,3 +418,46 @@ def test_agrees_with_the_dense_layer():
     want, tol = oplib.attention(q, k, v)
     oplib.check(dense[None], want["out"], tol["out"], "dense")
     oplib.check(out[None], want["out"], tol["out"], "out")
+
+
+@pytest.mark.parametrize("H,K,L,N,d,a,z", [
+    (2, 2, 100, 300, 64, 10, 50),             # one tile of queries
+    (4, 2, 300, 700, 40, 129, 131),           # several; the gap inside one step
+    (8, 1, 2, 900, 64, 1, 899),               # few rows
+    (1, 1, 2100, 2500, 64, 700, 1400),        # two groups of warps a block in dK/dV, whole steps in the gap
+    (2, 1, 300, 3500, 64, 95, 3000),          # in dQ
+    (1, 1, 2100, 3500, 24, 1000, 1100),       # in both
+])
+@pytest.mark.parametrize("order", ["halves", "in turn"])
+def test_a_gap_between_ranges_may_hold_anything(H, K, L, N, d, a, z, order):
+    """Queries of [0, a) beside queries of [z, N): NaN and infinities in the
+    keys and values between, which nobody sees, change no bit."""
+    q, k, v, dout = _inputs(1, H, K, L, N, d)
+    i = torch.arange(L, device="cuda")[None]
+    first = i < (L + 1) // 2 if order == "halves" else i % 2 == 0
+    b, e = torch.where(first, 0, z).int(), torch.where(first, a, N).int()
+    want = _run(q, k, v, dout, b, e)
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").bfloat16()
+    k, v = k.clone(), v.clone()
+    k[:, :, a:z] = v[:, :, a:z] = bad[torch.arange(d, device="cuda") % 3]
+    got = _run(q, k, v, dout, b, e)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("H,K,L,N,mask", [(2, 2, 300, 300, "causal"), (2, 1, 300, 700, "random"),
+                                          (1, 1, 2100, 3500, "window"), (1, 1, 600, 3500, "random")])
+def test_keys_reach_only_the_query_gradients_that_see_them(H, K, L, N, mask):
+    """NaN in a key: dq is NaN in the rows that see it, and the others keep
+    their bits."""
+    q, k, v, dout = _inputs(1, H, K, L, N, 64)
+    b, e = _ranges(mask, 1, L, N)
+    want = _run(q, k, v, dout, b, e)
+    j = N - N // 4
+    k = k.clone()
+    k[:, :, j] = float("nan")
+    got = _run(q, k, v, dout, b, e)
+    sees = ((b.clamp(0, N) <= j) & (j < e.clamp(0, N)))[0]
+    assert sees.any() and not sees.all()
+    assert torch.isnan(got["dq"][0][:, sees]).all()
+    assert torch.equal(got["dq"][0][:, ~sees], want["dq"][0][:, ~sees])

@@ -588,7 +588,7 @@ struct DqSmem {
   uint8_t k[kKvStages][kKeyBytes], v[kKvStages][kKeyBytes];
   uint64_t q_full, kv_full[kKvStages], kv_empty[kKvStages];
   uint64_t s_full[G], dp_full[G], s_read[G], ds_ready[G], drain, dirty, clean;
-  int lo[4], hi[4];
+  alignas(16) int lo[4], hi[4], f_lo[4], f_hi[4];
   uint32_t tmem_base;
   int abort;
 };
@@ -618,9 +618,12 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
   const bool live = keys.x < keys.y;
   if (warp >= 4 && warp < 8) {
     const int x = warp_min(live ? keys.x : 0x7fffffff), y = warp_max(live ? keys.y : 0);
+    const int fx = warp_max(live ? keys.x : 0), fy = warp_min(live ? keys.y : 0x7fffffff);
     if (lane == 0) {
       sm.lo[warp - 4] = x;
       sm.hi[warp - 4] = y;
+      sm.f_lo[warp - 4] = fx;
+      sm.f_hi[warp - 4] = fy;
     }
   }
   DevState* st = a.st;
@@ -759,6 +762,19 @@ attn_dq_kernel(const __grid_constant__ AttnMap mq, const __grid_constant__ AttnM
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&sm.s_read[grp]);
+      // (read again each step: every live row of the tile sees [f_lo, f_hi))
+      if (half == 0 && (max(max(sm.f_lo[0], sm.f_lo[1]), max(sm.f_lo[2], sm.f_lo[3])) > base + j * kKeyStep ||
+                        min(min(sm.f_hi[0], sm.f_hi[1]), min(sm.f_hi[2], sm.f_hi[3])) < min(base + (j + 1) * kKeyStep, hi))) {
+        // some row does not see all of this step, and its dS of 0 times an
+        // infinity or NaN there would not be 0: S has read K as it is, so
+        // rows that see such a key have their NaN in dS; dQ reads it without
+        const int s = j % kKvStages;
+        if (!wait_all(&sm.kv_full[s], (j / kKvStages) & 1, abort, st)) { ok = false; break; }
+        if (row < kKeyStep && wild_row(sm.k[s], row)) {
+          tame_row(sm.k[s], row);
+          fence_async_smem();
+        }
+      }
       const bool masked = f_lo > j * kKeyStep || f_hi < j * kKeyStep + kKeyCols;
 #pragma unroll
       for (int e = 0; e < kKeyCols / 2; ++e) exp2_pair(p[2 * e], p[2 * e + 1], cc, mm);
