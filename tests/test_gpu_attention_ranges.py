@@ -461,3 +461,26 @@ def test_keys_reach_only_the_query_gradients_that_see_them(H, K, L, N, mask):
     assert sees.any() and not sees.all()
     assert torch.isnan(got["dq"][0][:, sees]).all()
     assert torch.equal(got["dq"][0][:, ~sees], want["dq"][0][:, ~sees])
+
+
+@pytest.mark.parametrize("H,K,L,N", [(2, 2, 60, 4000), (1, 1, 1, 20000), (1, 1, 4, 60000), (1, 1, 9, 4000)])
+def test_nan_survives_the_join_of_split_keys(H, K, L, N):
+    """Where the keys of few rows are split: a NaN that is the only key a row
+    sees of a part, a whole part of NaN, and a query of NaN."""
+    q, k, v, _ = _inputs(1, H, K, L, N, 64)
+    for lo, hi, bad in [(0, j + 1, slice(j, j + 1)) for j in range(0, N, 96 if N < 5000 else 1024)] + \
+                       [(0, N, slice(N // 2, N)), (5, N, slice(5, N // 2))]:
+        b = torch.full((1, L), lo, dtype=torch.int32, device="cuda")
+        e = torch.full((1, L), hi, dtype=torch.int32, device="cuda")
+        if L > 1:
+            e[0, L // 2:] = N                 # the other rows keep the parts where they are
+        x = k.clone()
+        x[:, :, bad] = float("nan")
+        out, lse = ops.httm_attention_forward(q, x, v, b, e)
+        assert torch.isnan(out).all() and torch.isnan(lse).all(), (lo, hi, bad)
+    q = q.clone()
+    q[0, 0, L // 2] = float("nan")
+    out, lse = ops.httm_attention_forward(q, k, v)
+    rows = torch.arange(L, device="cuda") != L // 2
+    assert torch.isnan(out[0, 0, L // 2]).all() and torch.isnan(lse[0, 0, L // 2])
+    assert torch.isfinite(out[0, :, rows]).all() and torch.isfinite(lse[0, :, rows]).all()

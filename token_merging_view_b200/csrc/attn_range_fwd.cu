@@ -754,11 +754,13 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, int tile_rows, int row_tile
   for (int p = 0; p < parts; ++p) mx = fmaxf(mx, src[p * step + kAttnD + 1]);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p = 0; p < parts; ++p) {
-    const float m = src[p * step + kAttnD + 1];
-    if (m == -INFINITY) continue;                    // saw none of its keys
+    const float m = src[p * step + kAttnD + 1], l = src[p * step + kAttnD];
+    // saw none of its keys, and may have left no O.  (Maxima pass NaN over: a
+    // part whose scores are all NaN has this maximum too, and a sum of NaN.)
+    if (m == -INFINITY && l == 0.f) continue;
     const float w = ex2(m - mx);
     const float4 x = reinterpret_cast<const float4*>(src + p * step)[c];
-    sum = fmaf(src[p * step + kAttnD], w, sum);
+    sum = fmaf(l, w, sum);
     o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
   }
   const int l = r / a.G, head = (bk % a.K) * a.G + (r - l * a.G), b = bk / a.K;
