@@ -484,3 +484,25 @@ def test_nan_survives_the_join_of_split_keys(H, K, L, N):
     rows = torch.arange(L, device="cuda") != L // 2
     assert torch.isnan(out[0, 0, L // 2]).all() and torch.isnan(lse[0, 0, L // 2])
     assert torch.isfinite(out[0, :, rows]).all() and torch.isfinite(lse[0, :, rows]).all()
+
+
+@pytest.mark.parametrize("N", [3000, 40000])
+def test_cleaned_values_leave_later_keys_alone(N):
+    """Few rows: infinities and NaN in a channel of the values of every other
+    tile of 32 keys, all of which some row does not see; the loads that reuse
+    the cleaned tiles' memory bring the keys behind them whole."""
+    H, K, L, d = 4, 2, 3, 64
+    q, k, v, _ = _inputs(1, H, K, L, N, d)
+    b = torch.tensor([[0, N // 2, N - 40]], dtype=torch.int32, device="cuda")
+    e = torch.tensor([[N - 1, N, N]], dtype=torch.int32, device="cuda")
+    want, lse = ops.httm_attention_forward(q, k, v, b, e)
+    v = v.clone()
+    j = torch.arange(N, device="cuda")
+    odd = (j // 32 % 2 == 0) & (j < N - 40)
+    for i, x in enumerate((float("nan"), float("inf"), -float("inf"))):
+        v[:, :, odd & (j % 3 == i), 5] = x
+    for _ in range(20):
+        out, lse2 = ops.httm_attention_forward(q, k, v, b, e)
+        rest = torch.arange(d, device="cuda") != 5
+        assert torch.equal(lse, lse2) and torch.equal(out[..., rest], want[..., rest])
+        assert torch.isnan(out[0, :, :2, 5]).all() and torch.equal(out[0, :, 2, 5], want[0, :, 2, 5])

@@ -182,7 +182,10 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
     // are added below to the rows that see them
     const bool mixed = k0 < f_lo || min(k0 + kKeys, hi) > f_hi;
     const uint32_t odd = mixed ? __ballot_sync(0xffffffffu, wild_row(vs, lane)) : 0u;
-    if (odd >> lane & 1) tame_row(vs, lane);
+    if (odd >> lane & 1) {
+      tame_row(vs, lane);
+      fence_async_smem();                             // before the TMA load that reuses this stage
+    }
     __syncwarp();
     const uint32_t ka = smem_u32(ks), va = smem_u32(vs);
 #pragma unroll
