@@ -484,7 +484,8 @@ typedef struct {
 } httm_attention;
 
 /* Workspace bytes of the two calls (host only; either output may be NULL).
- * The workspace is 256-byte aligned device memory; 0 bytes: NULL will do. */
+ * They depend on the extents alone: key_begin and key_end are not looked at,
+ * and the bytes do for calls with ranges and without.  The workspace is 256-byte aligned device memory; 0 bytes: NULL will do. */
 httm_status httm_attention_workspace_bytes(const httm_attention* a, size_t* forward, size_t* backward);
 
 /*

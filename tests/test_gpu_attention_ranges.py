@@ -506,3 +506,20 @@ def test_cleaned_values_leave_later_keys_alone(N):
         rest = torch.arange(d, device="cuda") != 5
         assert torch.equal(lse, lse2) and torch.equal(out[..., rest], want[..., rest])
         assert torch.isnan(out[0, :, :2, 5]).all() and torch.equal(out[0, :, 2, 5], want[0, :, 2, 5])
+
+
+@pytest.mark.parametrize("B,H,K,L,N", [(16, 1, 1, 1, 8192), (4, 16, 4, 1, 8192), (1, 16, 16, 2, 4000), (1, 2, 2, 60, 4000)])
+def test_a_workspace_of_the_extents_serves_calls_with_ranges(B, H, K, L, N):
+    q, k, v, dout = _inputs(B, H, K, L, N, 64)
+    need_f, need_b = ops.httm_attention_workspace_bytes(B, H, K, L, N, 64)
+    guard = 4096
+    for b, e in ((None, None), ops.causal_ranges(B, L, N), ops.causal_ranges(B, L, N, window=N // 3)):
+        want = _run(q, k, v, dout, b, e)
+        ws = torch.full((max(need_f, need_b) + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+        out, lse = ops.httm_attention_forward(q, k, v, b, e, workspace=ws[:need_f])
+        assert torch.equal(out, want["out"]) and torch.equal(lse, want["lse"]) and (ws[need_f:] == 0xA5).all()
+        ws.fill_(0xA5)
+        grads = ops.httm_attention_backward(dout, q, k, v, out, lse, b, e, workspace=ws[:need_b])
+        assert (ws[need_b:] == 0xA5).all()
+        for n, t in zip(("dq", "dk", "dv"), grads):
+            assert torch.equal(t, want[n]), n

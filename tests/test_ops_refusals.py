@@ -211,3 +211,15 @@ def test_ranges_and_frequencies_on_the_host():
     assert y[0] == full[0] and abs(float(y[-1] * 8 / full[-1]) - 1) < 1e-12 and factor > 1
     with pytest.raises(ValueError):
         ops.rotary_frequencies(4, scaling="cubic", device="cpu")
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,q_len,kv_len", [
+    (16, 1, 1, 1, 8192), (4, 16, 4, 1, 8192), (64, 1, 1, 1, 32768), (1, 16, 16, 1, 1369), (1, 16, 16, 2, 4000),
+    (1, 2, 2, 60, 4000), (3, 8, 1, 4, 100000), (1, 1, 1, 33, 9000)])
+def test_attention_workspace_depends_on_the_extents_alone(batch, heads, kv_heads, q_len, kv_len):
+    """The same bytes with key ranges and without, so that a workspace sized
+    from the extents serves both."""
+    args = (batch, heads, kv_heads, q_len, kv_len, 64)
+    plain = ops.httm_attention_workspace_bytes(*args)
+    for begin, end in ((0, FAKE), (FAKE, 0), (FAKE, FAKE)):
+        assert ops._attention_bytes(ops.httm_attention(*args, 0, 0.0, begin, end)) == plain

@@ -44,8 +44,9 @@ struct AttnFwdPlan {
   long long items;                      // B * K * row_tiles
   size_t part_bytes;
 };
-AttnFwdPlan attn_fwd_plan(const httm_attention& a);
-int attn_rows_parts(const httm_attention& a);
+// `ranges`: are there key ranges (few rows are split otherwise then)?
+AttnFwdPlan attn_fwd_plan(const httm_attention& a, bool ranges);
+int attn_rows_parts(const httm_attention& a, bool ranges);
 cudaError_t launch_attn_rows(const AttnArgs& a, const AttnFwdPlan& p, float* part_out, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnFwdPlan& p, void* ws, cudaStream_t s);
 

@@ -110,7 +110,10 @@ extern "C" {
 httm_status httm_attention_workspace_bytes(const httm_attention* a, size_t* forward, size_t* backward) {
   HTTM_TRY(check_attention(a));
   const bool none = a->batch == 0;
-  if (forward) *forward = none || a->q_len == 0 ? 0 : attn_fwd_plan(*a).part_bytes;
+  // enough for calls with key ranges and without
+  if (forward)
+    *forward = none || a->q_len == 0
+                   ? 0 : std::max(attn_fwd_plan(*a, true).part_bytes, attn_fwd_plan(*a, false).part_bytes);
   if (backward) *backward = none ? 0 : attn_bwd_plan(*a).total;
   return HTTM_OK;
 }
@@ -126,7 +129,7 @@ httm_status httm_attention_forward(const httm_attention* a, const httm_view* q, 
   HTTM_TRY(check_view(out, g.B, g.H, g.L, g.d, true, &g.out));
   if (!aligned(lse, 4) || !aligned(g.kb, 4) || !aligned(g.ke, 4)) return HTTM_ERR_ALIGN;
   if (g.B == 0 || g.L == 0) return HTTM_OK;
-  const AttnFwdPlan p = attn_fwd_plan(*a);
+  const AttnFwdPlan p = attn_fwd_plan(*a, a->key_begin || a->key_end);
   if (p.part_bytes && (!workspace || workspace_bytes < p.part_bytes)) return HTTM_ERR_WORKSPACE;
   if (p.part_bytes && !aligned(workspace, 256)) return HTTM_ERR_ALIGN;
   g.lse = lse;

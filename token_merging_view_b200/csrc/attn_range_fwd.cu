@@ -813,7 +813,7 @@ void split(const httm_attention& a, bool pair, AttnFwdPlan* p) {
 // 64 x 128 tokens 52 and 35 us, 32 x 256 47 and 41, 8 x 1,369 149 and 127,
 // 2 x 2,738 131 and 111, 8,214 423 and 421, 16,384 1345 and 1390; split, 64
 // rows on 8,000 keys 20.9 and 22.4.
-AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
+AttnFwdPlan attn_fwd_plan(const httm_attention& a, bool ranges) {
   AttnFwdPlan p{};
   p.rows = a.q_len * (a.heads / a.kv_heads);
   p.few = p.rows <= kAttnFewRows;
@@ -821,7 +821,7 @@ AttnFwdPlan attn_fwd_plan(const httm_attention& a) {
     p.tile_rows = 2 * kAttnTile;
     p.row_tiles = 1;
     p.items = (long long)a.batch * a.kv_heads;
-    p.parts = attn_rows_parts(a);
+    p.parts = attn_rows_parts(a, ranges);
   } else {
     if (a.kv_len <= 8192) split(a, true, &p);
     if (a.kv_len > 8192 || p.parts > 1) split(a, false, &p);

@@ -372,10 +372,9 @@ attn_rows_kernel(const __grid_constant__ AttnMap mk, const __grid_constant__ Att
 // so the items are cut in enough parts to even out.  Up to kCluster parts
 // cost little to add up (rounded to a power of two: clusters of other sizes
 // leave SMs idle); beyond that the join is a launch of its own.
-int attn_rows_parts(const httm_attention& a) {
+int attn_rows_parts(const httm_attention& a, bool ranges) {
   const long long items = (long long)a.batch * a.kv_heads, rounds = (a.kv_len + kWarps * kKeys - 1) / (kWarps * kKeys);
   const int slots = 2 * kSMs;
-  const bool ragged = a.key_end || a.key_begin;
   const int most = (int)std::min<long long>(kAttnMaxParts, std::max<long long>(1, rounds));
   int parts = 1;
   double best = 0;
@@ -385,7 +384,7 @@ int attn_rows_parts(const httm_attention& a) {
     const long long waves = (items * n + slots - 1) / slots;
     double cost = (double)waves * ((rounds + n - 1) / n + 4) + (n > kCluster ? 4 + n / 8.0 : n > 1 ? 1 : 0);
     // ragged items: the longest part bounds the last wave
-    if (ragged && waves < 4) cost += (double)(rounds + n - 1) / n * (4 - waves) / 4;
+    if (ranges && waves < 4) cost += (double)(rounds + n - 1) / n * (4 - waves) / 4;
     if (best == 0 || cost < best) best = cost, parts = n;
   }
   return parts;

@@ -150,7 +150,8 @@ def _attention(q, k, v, key_begin, key_end, softmax_scale):
 
 
 def httm_attention_workspace_bytes(batch, heads, kv_heads, q_len, kv_len, d_head, dtype=torch.bfloat16):
-    """(forward, backward) workspace bytes; no device call."""
+    """(forward, backward) workspace bytes of calls of these sizes, with key
+    ranges or without; no device call."""
     return _attention_bytes(httm_attention(batch, heads, kv_heads, q_len, kv_len, d_head, _DTYPES[dtype], 0.0, 0, 0))
 
 
