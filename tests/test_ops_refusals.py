@@ -4,6 +4,9 @@ the Python functions refuse tensors before any pointer leaves them."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -223,3 +226,15 @@ def test_attention_workspace_depends_on_the_extents_alone(batch, heads, kv_heads
     plain = ops.httm_attention_workspace_bytes(*args)
     for begin, end in ((0, FAKE), (FAKE, 0), (FAKE, FAKE)):
         assert ops._attention_bytes(ops.httm_attention(*args, 0, 0.0, begin, end)) == plain
+
+
+def test_package_imports_on_a_torch_without_cuda():
+    """Host-only use (planning, sizes) needs none of torch's CUDA bindings."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "import token_merging_view_b200 as p\n"
+            "assert p.httm_attention_workspace_bytes(1, 2, 2, 100, 100, 64)[1] > 0\n"
+            "assert p.causal_ranges(1, 2, 2, device='cpu')[1].tolist() == [[1, 2]]\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

@@ -38,8 +38,11 @@ httm_norm_cfg = Struct("@q6i3f0q").pack     # rows, channels .. gates, post_eps,
 httm_rows = Struct("@Pq").pack              # data, row stride
 httm_norm_weights = httm_norm_grads = Struct("@5P").pack   # in the order of _PARAMS
 
-_device_of_thread = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current device and raw stream, the short way where this torch has one (a
+# torch without CUDA has not, and can still import the package and plan).
+_device_of_thread = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _data(t):
