@@ -238,3 +238,19 @@ def test_package_imports_on_a_torch_without_cuda():
     r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("device,index", [(None, 3), ("cuda", 3), (torch.device("cuda"), 3), ("cuda:1", 1), (0, 0),
+                                          (torch.device("cuda", 2), 2)])
+def test_device_status_reads_the_device_that_is_meant(device, index, monkeypatch):
+    class Seen(Exception):
+        pass
+
+    def on(i, stream):
+        raise Seen(i)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(ops, "_On", on)
+    with pytest.raises(Seen) as seen:
+        ops.httm_ops_device_status(device)
+    assert seen.value.args == (index,)

@@ -478,7 +478,9 @@ def httm_gated_norm_backward(dy, dz, f, y, stats, gate=None, post=None, pre=None
 def httm_ops_device_status(device=None, stream=None) -> int:
     """Synchronises the stream; returns the HTTM_DEV_* bits the operators'
     kernels set on the device since the last call (0 = clean)."""
-    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    index = None if device is None else torch.device(device).index
+    if index is None:                                # none, or "cuda": the current one
+        index = torch.cuda.current_device()
     v = ctypes.c_uint32(0)
     with _On(index, stream) as s:
         st = load_library().httm_ops_device_status(s, ctypes.byref(v))
