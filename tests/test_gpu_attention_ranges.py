@@ -523,3 +523,55 @@ def test_a_workspace_of_the_extents_serves_calls_with_ranges(B, H, K, L, N):
         assert (ws[need_b:] == 0xA5).all()
         for n, t in zip(("dq", "dk", "dv"), grads):
             assert torch.equal(t, want[n]), n
+
+
+@pytest.mark.parametrize("G,L,N,mask", [(1, 600, 5000, "random"), (1, 18900, 5000, "random"), (2, 9500, 9000, "random"),
+                                        (2, 300, 20000, "random"), (1, 700, 700, "causal"), (4, 5, 9000, "random")])
+def test_scattered_infinities_reach_exactly_the_rows_that_see_them(G, L, N, mask):
+    """One value in 2,000 an infinity or NaN: a row and channel that sees none
+    keeps its bits; else it is what the seen ones add up to."""
+    K, d = 2, 64
+    q, k, v, _ = _inputs(1, K * G, K, L, N, d)
+    b, e = _ranges(mask, 1, L, N)
+    want, lse = ops.httm_attention_forward(q, k, v, b, e)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    kind = torch.randint(0, 6000, v.shape, generator=g, device="cuda")
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").bfloat16()
+    v = torch.where(kind < 3, bad[kind.clamp(max=2)], v)
+    out, lse2 = ops.httm_attention_forward(q, k, v, b, e)
+    assert torch.equal(lse, lse2)
+    lo, hi = b.long().clamp(0, N)[0], e.long().clamp(0, N)[0]
+    hi = torch.maximum(lo, hi)
+    seen = []
+    for x in range(3):                        # [kv_heads, L, d]: does the row see one of them?
+        n = torch.nn.functional.pad((kind[0] == x).int().cumsum(1), (0, 0, 1, 0))
+        seen.append((n[:, hi] - n[:, lo] > 0).repeat_interleave(G, 0))
+    nan, pos, neg = seen[0] | seen[1] & seen[2], seen[1], seen[2]
+    got = out[0]
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got == float("inf"), pos & ~nan) and torch.equal(got == -float("inf"), neg & ~nan)
+    rest = ~(nan | pos | neg)
+    assert torch.equal(got[rest], want[0][rest])
+
+
+def test_a_nan_value_does_not_cost_a_walk_over_all_values():
+    """Device time of a causal call with two NaN values against one without
+    (walking every key a row sees took 44 times as long, the marked ones 2)."""
+    q, k, v, _ = _inputs(1, 1, 1, 4096, 4096, 64)
+    b, e = ops.causal_ranges(1, 4096, 4096)
+    bad = v.clone()
+    bad[:, :, 50] = bad[:, :, 3996] = float("nan")
+
+    def best(x):
+        times = []
+        for _ in range(10):
+            t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            t0.record()
+            for _ in range(5):
+                ops.httm_attention_forward(q, k, x, b, e)
+            t1.record()
+            t1.synchronize()
+            times.append(t0.elapsed_time(t1))
+        return min(times)
+
+    assert best(bad) < 8 * best(v)

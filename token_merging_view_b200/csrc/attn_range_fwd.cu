@@ -47,6 +47,14 @@ constexpr int kAuxRegs = 88, kSoftmaxRegs = 208;   // of 384 x 168 at launch
 constexpr uint32_t kColO = 384;           // O_t at kColO + 64 t; S ring at 0, 128, 256
 constexpr int kPartStride = httm::kAttnRangePart;
 
+// Where V held infinities or NaN in a tile with masks: mark i is set for some
+// of the part's keys i, i + kWildMarks, ...
+constexpr int kWildMarks = 4096;          // 16 a thread of the smaller block
+struct WildKeys {
+  alignas(16) uint8_t mark[kWildMarks];
+  int any;
+};
+
 struct FwdSmem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kStages][kTileBytes];
@@ -56,28 +64,42 @@ struct FwdSmem {
   uint64_t s_full[3], p_full[2], o_done[2];
   uint64_t drain, dirty, clean;
   int lo[8], hi[8], f_lo[8], f_hi[8];
-  int wild;                              // V held infinities or NaN in a tile with masks
   uint32_t tmem_base;
   int abort;
+  WildKeys wild;
 };
 constexpr size_t kSmemBytes = sizeof(FwdSmem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// Adds the infinities and NaN of the values [key, last) of a key head to an
-// output row in memory.
+// Adds the infinities and NaN of the marked values, `n` keys of the part from
+// `base` on, to the output row of a thread that sees `keys`.  A warp's lanes
+// walk together, so that their loads are broadcasts; out of line, where it
+// costs the kernel no registers.
 template <class T>
-__device__ __noinline__ void add_wild(const AttnArgs& a, int b, int kh, int key, int last, T* row) {
-  for (; key < last; ++key) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.v.data) +
-                                                            b * a.v.sb + kh * a.v.sh + (int64_t)key * a.v.st);
-    for (int c = 0; c < a.d / 2; ++c) {
-      const uint32_t x = src[c];
-      if (!wild(x)) continue;
-      for (int e = 0; e < 2; ++e) {
-        const float v = __uint_as_float(e ? x & 0xffff0000u : x << 16);
-        if (!isfinite(v)) row[2 * c + e] = from_f<T>(to_f(row[2 * c + e]) + v);
-      }
+__device__ __noinline__ void add_wild(const AttnArgs& a, int b, int kh, const WildKeys& w, int base, int n, int2 keys,
+                                      T* row) {
+  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v.data) + b * a.v.sb + kh * a.v.sh;
+  const int end = min(base + n, a.N);
+  for (int c = 0; c < a.d; c += 8) {
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < min(n, kWildMarks); i += 16) {
+      const uint4 marks = *reinterpret_cast<const uint4*>(w.mark + i);
+      if ((marks.x | marks.y | marks.z | marks.w) == 0u) continue;
+      for (int at = i; at < i + 16; ++at)
+        for (int key = w.mark[at] ? base + at : end; key < end; key += kWildMarks) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + (int64_t)key * a.v.st + c);
+          if (!wild(x) || key < keys.x || key >= keys.y) continue;
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float f = __uint_as_float((e & 1) ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+            if (!isfinite(f)) sum[e] += f;
+          }
+        }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!isfinite(sum[e])) row[c + e] = from_f<T>(to_f(row[c + e]) + sum[e]);
   }
 }
 
@@ -97,10 +119,10 @@ __device__ __forceinline__ void load_query_row(const AttnArgs& a, uint8_t* tile,
 
 // A finished row: to `part` its unnormalised sums, the row sum and the
 // maximum in use, or (part null) the output and its log-sum-exp.  `o` is its O
-// if it has any; `wild_end`: see add_wild.
+// if it has any; `w`: see add_wild.
 __device__ __forceinline__ void finish_row(const AttnArgs& a, int b, int kh, int head, int l, bool in_item, bool live,
                                            bool any, const uint32_t (&o)[64], float sum, float m_used, float* part,
-                                           int wild_key, int wild_end) {
+                                           const WildKeys& w, int base, int n, int2 keys) {
   if (!in_item) return;
   if (part) {
     if (any) {
@@ -111,7 +133,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int b, int kh, int
     }
     part[kAttnD] = sum;
     part[kAttnD + 1] = m_used;
-    if (wild_end) add_wild(a, b, kh, wild_key, wild_end, part);
+    if (w.any) add_wild(a, b, kh, w, base, n, keys, part);
     return;
   }
   __nv_bfloat16* dst =
@@ -123,7 +145,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int b, int kh, int
   } else {
     for (int v = 0; v < a.d / 8; ++v) reinterpret_cast<uint4*>(dst)[v] = make_uint4(0, 0, 0, 0);
   }
-  if (wild_end) add_wild(a, b, kh, wild_key, wild_end, dst);
+  if (w.any) add_wild(a, b, kh, w, base, n, keys, dst);
   if (a.lse)
     a.lse[((size_t)b * a.H + head) * a.L + l] = live ? (m_used + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
@@ -176,10 +198,11 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
     mbar_init(&sm.dirty, 1);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
-    sm.wild = 0;
+    sm.wild.any = 0;
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc(&sm.tmem_base, 512);
+  if (threadIdx.x < kWildMarks / 16) reinterpret_cast<uint4*>(sm.wild.mark)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -311,7 +334,8 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
             // tile 0's product with this V comes first and takes it as it
             // is; tile 1's comes behind both tiles' P, so it sees the note
             if (t == 1) mbar_wait(&sm.o_done[0], j & 1, abort, st);
-            sm.wild = 1;
+            sm.wild.mark[(k0 + row) % kWildMarks] = 1;
+            sm.wild.any = 1;
             tame_row(sm.v[s], row);
             fence_async_smem();
           }
@@ -421,11 +445,11 @@ attn_range_fwd_kernel(const __grid_constant__ AttnMap mk, const __grid_constant_
       if (ok) {
         uint32_t o[64];
         if (n_kv > 0) tmem_ld64(to, o);
-        const int wild_end = sm.wild && live ? min(keys.y, base + n_kv * kAttnTile) : 0;
         float* part_row =
             parts > 1 ? part_out + ((size_t)blockIdx.x * min(a.L * a.G, 256) + (in_item ? r_item : 0)) * kPartStride
                       : nullptr;
-        finish_row(a, b, kh, head, l, in_item, live, n_kv > 0, o, sum, m_used, part_row, max(keys.x, base), wild_end);
+        finish_row(a, b, kh, head, l, in_item, live, n_kv > 0, o, sum, m_used, part_row, sm.wild, base, n_kv * kAttnTile,
+                   keys);
       }
     }
   }
@@ -462,9 +486,9 @@ struct PairSmem {
   uint64_t q_full, kv_full[kPairStages], kv_empty[kPairStages];
   uint64_t s_full[2], p_full[2], o_done[2], drain, dirty, clean;
   int lo[4], hi[4], f_lo[4], f_hi[4];
-  int wild;
   uint32_t tmem_base;
   int abort;
+  WildKeys wild;
 };
 constexpr size_t kPairSmem = sizeof(PairSmem) + 1024;
 static_assert(2 * (kPairSmem + 1024) <= 227 * 1024, "two blocks an SM");
@@ -513,10 +537,11 @@ attn_range_pair_kernel(const __grid_constant__ AttnMap mk, const __grid_constant
     mbar_init(&sm.dirty, 1);
     mbar_init(&sm.clean, 1);
     sm.abort = 0;
-    sm.wild = 0;
+    sm.wild.any = 0;
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc(&sm.tmem_base, 256);
+  if (threadIdx.x < kWildMarks / 16) reinterpret_cast<uint4*>(sm.wild.mark)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -624,7 +649,8 @@ attn_range_pair_kernel(const __grid_constant__ AttnMap mk, const __grid_constant
         const int s = j % kPairStages;
         if (!wait_all(&sm.kv_full[s], (j / kPairStages) & 1, abort, st)) { ok = false; break; }
         if (row < kPairKeys && wild_row(sm.v[s], row)) {
-          sm.wild = 1;
+          sm.wild.mark[(k0 + row) % kWildMarks] = 1;
+          sm.wild.any = 1;
           tame_row(sm.v[s], row);
           fence_async_smem();
         }
@@ -719,10 +745,9 @@ attn_range_pair_kernel(const __grid_constant__ AttnMap mk, const __grid_constant
     if (ok) {
       uint32_t o[64];
       if (n > 0) tmem_ld64(to, o);
-      const int wild_end = sm.wild && live ? min(keys.y, base + n * kPairKeys) : 0;
       float* part_row = parts > 1 ? part_out + ((size_t)blockIdx.x * min(a.L * a.G, kAttnTile) + (in_item ? row : 0)) * kPartStride
                                   : nullptr;
-      finish_row(a, b, kh, head, l, in_item, live, n > 0, o, sum, m_used, part_row, max(keys.x, base), wild_end);
+      finish_row(a, b, kh, head, l, in_item, live, n > 0, o, sum, m_used, part_row, sm.wild, base, n * kPairKeys, keys);
     }
   }
 
