@@ -575,3 +575,13 @@ def test_a_nan_value_does_not_cost_a_walk_over_all_values():
         return min(times)
 
     assert best(bad) < 8 * best(v)
+
+
+@pytest.mark.parametrize("H,K,L,N,d,mask", [(2, 2, 40, 1369, 64, "none"), (16, 4, 64, 1369, 64, "causal"),
+                                            (16, 4, 317, 2738, 40, "random"), (3, 1, 200, 8192, 64, "window"),
+                                            (2, 1, 130, 5000, 64, "packed"), (6, 2, 34, 1500, 8, "padded")])
+def test_split_keys_of_mid_sized_calls(H, K, L, N, d, mask):
+    """Up to 8,192 keys and too few query rows to fill the SMs: the keys are
+    split among blocks that share an SM, and joined."""
+    assert ops.httm_attention_workspace_bytes(1, H, K, L, N, d)[0] > 0
+    test_against_definition((1, H, K, L, N, d, mask))

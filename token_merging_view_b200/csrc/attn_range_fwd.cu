@@ -833,11 +833,14 @@ void split(const httm_attention& a, bool pair, AttnFwdPlan* p) {
 }
 }  // namespace
 
-// Which kernel: the pair kernel up to 8,192 keys, unless it would need a
-// split to fill the SMs.  Measured with 16 heads, large kernel against pair:
-// 64 x 128 tokens 52 and 35 us, 32 x 256 47 and 41, 8 x 1,369 149 and 127,
-// 2 x 2,738 131 and 111, 8,214 423 and 421, 16,384 1345 and 1390; split, 64
-// rows on 8,000 keys 20.9 and 22.4.
+// Which kernel: the pair kernel up to 8,192 keys.  Measured with 16 heads,
+// large kernel against pair: 64 x 128 tokens 52 and 35 us, 32 x 256 47 and 41,
+// 8 x 1,369 149 and 127, 2 x 2,738 131 and 111, 8,214 423 and 421, 16,384 1345
+// and 1390.  Split (one sequence): 64 queries on 1,369 keys 14.8 and 13.1, on
+// 8,000 20.9 and 22.5; 317 on 2,738 25.0 and 20.5, on 8,000 39.7 and 31.8; with
+// 4 key heads 64 on 1,369 20.0 and 13.9, on 8,000 27.2 and 20.5.  Over 34 to
+// 1,000 queries on 500 to 8,000 keys the large one is 12 % behind in the mean,
+// 44 % at most, and at most 15 % ahead (64 on 5,476, 18.5 and 21.3).
 AttnFwdPlan attn_fwd_plan(const httm_attention& a, bool ranges) {
   AttnFwdPlan p{};
   p.rows = a.q_len * (a.heads / a.kv_heads);
@@ -848,8 +851,7 @@ AttnFwdPlan attn_fwd_plan(const httm_attention& a, bool ranges) {
     p.items = (long long)a.batch * a.kv_heads;
     p.parts = attn_rows_parts(a, ranges);
   } else {
-    if (a.kv_len <= 8192) split(a, true, &p);
-    if (a.kv_len > 8192 || p.parts > 1) split(a, false, &p);
+    split(a, a.kv_len <= 8192, &p);
   }
   p.part_bytes = p.parts > (p.few ? kAttnCluster : 1)
                      ? (size_t)p.items * p.parts * std::min(p.rows, p.tile_rows) * kPartStride * 4 : 0;
