@@ -639,6 +639,17 @@ httm_status httm_gated_norm_backward(const httm_norm_cfg* c, const httm_norm_wei
  */
 httm_status httm_ops_device_status(void* stream, uint32_t* status);
 
+/*
+ * The bound, in nanoseconds, of every device wait of the operators on the
+ * current device (2e9 to begin with), for what is launched on `stream` from
+ * here on and for other streams once this has run.  A wait that runs out sets
+ * HTTM_DEV_TIMEOUT; its CTA stops its work, waits (with a fixed bound) for
+ * what it has in flight, frees its tensor memory and exits.  0 makes every
+ * wait run out that the hardware does not bridge by itself (some
+ * microseconds): a failure-detection check, not a setting for real work.
+ */
+httm_status httm_ops_set_wait_budget(uint64_t nanoseconds, void* stream);
+
 const char* httm_status_str(httm_status s);
 
 /*

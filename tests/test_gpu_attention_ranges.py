@@ -585,3 +585,34 @@ def test_split_keys_of_mid_sized_calls(H, K, L, N, d, mask):
     split among blocks that share an SM, and joined."""
     assert ops.httm_attention_workspace_bytes(1, H, K, L, N, d)[0] > 0
     test_against_definition((1, H, K, L, N, d, mask))
+
+
+@pytest.mark.parametrize("B,H,K,L,N", [
+    (1, 2, 2, 19000, 9000),                    # whole items, more than 8,192 keys
+    (1, 1, 1, 300, 200000),                    # split
+    (2, 4, 2, 1000, 1400),                     # two blocks an SM
+    (16, 16, 16, 1, 41070),                    # few rows, parts added up inside a cluster
+    (32, 16, 4, 1, 41070),                     # ... through the workspace
+])
+def test_waits_that_run_out_set_the_status_and_the_context_recovers(B, H, K, L, N):
+    """Failure detection without a fault: with no budget the first waits that
+    the hardware does not bridge by itself (some microseconds; the calls are
+    long enough) give up, the status says so, the kernels free what they hold
+    and exit; with the usual budget the same calls give the same bits as
+    before."""
+    from token_merging_view_b200 import binding
+    q, k, v, dout = _inputs(B, H, K, L, N, 64)
+    b, e = ops.causal_ranges(B, L, N)
+    want = _run(q, k, v, dout, b, e)
+    for call in (lambda: ops.httm_attention_forward(q, k, v, b, e),
+                 lambda: ops.httm_attention_backward(dout, q, k, v, want["out"], want["lse"], b, e)):
+        try:
+            ops.httm_ops_set_wait_budget(0)
+            call()
+            assert ops.httm_ops_device_status() & binding.HTTM_DEV_TIMEOUT
+        finally:
+            ops.httm_ops_set_wait_budget(2_000_000_000)
+        assert ops.httm_ops_device_status() == 0
+        again = _run(q, k, v, dout, b, e)
+        for n in want:
+            assert torch.equal(again[n], want[n]), n

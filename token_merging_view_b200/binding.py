@@ -31,7 +31,7 @@ EXPORTS = (
     "httm_plan_partition",
     "httm_attention_workspace_bytes", "httm_attention_forward", "httm_attention_backward", "httm_rotary",
     "httm_gated_norm_forward", "httm_gated_norm_workspace_bytes", "httm_gated_norm_backward",
-    "httm_ops_device_status",
+    "httm_ops_device_status", "httm_ops_set_wait_budget",
 )
 STAGES = ("match", "merge", "outlier", "attention", "unmerge", "other")
 
@@ -131,9 +131,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.httm_gated_norm_workspace_bytes.argtypes = [P, P]
     lib.httm_gated_norm_backward.argtypes = [P] * 11 + [S, V]
     lib.httm_ops_device_status.argtypes = [V, ctypes.POINTER(U)]
+    lib.httm_ops_set_wait_budget.argtypes = [ctypes.c_uint64, V]
     for name in ("httm_attention_workspace_bytes", "httm_attention_forward", "httm_attention_backward", "httm_rotary",
                  "httm_gated_norm_forward", "httm_gated_norm_workspace_bytes", "httm_gated_norm_backward",
-                 "httm_ops_device_status"):
+                 "httm_ops_device_status", "httm_ops_set_wait_budget"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

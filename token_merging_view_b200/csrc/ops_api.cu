@@ -11,6 +11,8 @@ namespace {
 // every device wait.
 __device__ DevState g_ops_state = {0, 0, 0, 0, {0, 0, 0, 0, 0, 0, 0, 0}, 0, 0, 0, 0, 0, 2000000000ull};
 
+__global__ void set_wait_kernel(DevState* st, unsigned long long ns) { st->wait_ns = ns; }
+
 }  // namespace
 
 DevState* ops_state() {
@@ -34,6 +36,15 @@ DevState* ops_state() {
 }  // namespace httm
 
 using namespace httm;
+
+extern "C" httm_status httm_ops_set_wait_budget(uint64_t nanoseconds, void* stream) {
+  DevState* st = ops_state();
+  if (!st) return cuda_fail(cudaGetLastError(), "ops_state");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  set_wait_kernel<<<1, 1, 0, s>>>(st, nanoseconds);
+  HTTM_OPS_LAUNCH(cudaGetLastError(), s);
+  return HTTM_OK;
+}
 
 extern "C" httm_status httm_ops_device_status(void* stream, uint32_t* status) {
   if (!status) return HTTM_ERR_ARG;

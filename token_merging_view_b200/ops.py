@@ -475,15 +475,27 @@ def httm_gated_norm_backward(dy, dz, f, y, stats, gate=None, post=None, pre=None
     return dict(dx=dx, df=df, **{"d" + name: t for name, t in zip(_PARAMS, grads)})
 
 
+def _index(device):
+    index = None if device is None else torch.device(device).index
+    return torch.cuda.current_device() if index is None else index   # none, or "cuda": the current one
+
+
 def httm_ops_device_status(device=None, stream=None) -> int:
     """Synchronises the stream; returns the HTTM_DEV_* bits the operators'
     kernels set on the device since the last call (0 = clean)."""
-    index = None if device is None else torch.device(device).index
-    if index is None:                                # none, or "cuda": the current one
-        index = torch.cuda.current_device()
     v = ctypes.c_uint32(0)
-    with _On(index, stream) as s:
+    with _On(_index(device), stream) as s:
         st = load_library().httm_ops_device_status(s, ctypes.byref(v))
     if st not in (0, 7, 8):
         _check(st, "httm_ops_device_status")
     return int(v.value)
+
+
+def httm_ops_set_wait_budget(nanoseconds, device=None, stream=None) -> None:
+    """Bounds every device wait of the operators on the device, from here on
+    in the stream's order (2e9 to begin with; 0: whatever is not complete
+    already runs out, to check the detection)."""
+    if not 0 <= nanoseconds < 2 ** 64:
+        raise ValueError("nanoseconds must be within 0 .. 2^64 - 1")
+    with _On(_index(device), stream) as s:
+        _check(load_library().httm_ops_set_wait_budget(nanoseconds, s), "httm_ops_set_wait_budget")
