@@ -144,3 +144,22 @@ def test_refusals():
         ops.httm_rotary(x, None, freqs, pos, q_out=torch.zeros((2, 1, 8, 64), device="cuda").expand(2, 4, 8, 64))
     with pytest.raises(ValueError, match="requires grad"):
         ops.httm_rotary(x.clone().requires_grad_(), None, freqs, pos)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_angles_are_as_good_near_quarter_turns_as_near_zero(sign):
+    """(1, 0) turned is (cos, sin): each within 6 roundings of itself (the
+    angle behind the nearest quarter turn is rounded once, and moves sine or
+    cosine by less than that relative to the value; 4 are the function's, at
+    most 2 steps; 1 the result's) and what 64 bits lose of position *
+    frequency, 2^-50 of it."""
+    pairs, T = 4, 200000
+    freqs = torch.tensor([1.0, 0.37, 2.0 ** -9 * 3.141592653589793, 1e-5], dtype=torch.float64, device="cuda")
+    x = torch.zeros((1, 1, T, 2 * pairs), device="cuda")
+    x[..., :pairs] = 1.0
+    pos = (sign * torch.arange(T, device="cuda")).int()
+    out, _ = ops.httm_rotary(x, None, freqs, pos, layout=HALF)
+    ang = pos.double()[:, None] * freqs
+    want = torch.cat([torch.cos(ang), torch.sin(ang)], -1)
+    bound = 6 * 2.0 ** -24 * want.abs() + 2.0 ** -50 * ang.abs().repeat(1, 2) + 2.0 ** -60
+    assert ((out[0, 0].double() - want).abs() <= bound).all()

@@ -10,9 +10,10 @@
 //
 // Angles: frequencies are given in radians per position (fp64).  In turns
 // and 64-bit fixed point, position * frequency is one integer product whose
-// overflow drops whole turns exactly; what is left is the fp64 rounding of
-// the frequency itself (2^-53 of it, times the position) and 2^-33 turns
-// from keeping the top 32 bits.
+// overflow drops whole turns exactly, and so do its top bits the quarters.
+// What is left is the fp64 rounding of the frequency in turns (2^-52 of it,
+// times the position) and the fp32 rounding of the rest, an eighth of a turn
+// at most: 2^-28 turns.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -85,10 +86,17 @@ __device__ __forceinline__ void turn(double freq, int pos, float factor, bool in
   const double t = freq * 0.15915494309189533577;            // 1 / (2 pi)
   const double frac = t - floor(t);
   const unsigned long long step = __double2ull_rn(frac * 18446744073709551616.0);   // 1.0 saturates to 2^64 - 1
-  const long long phase = (long long)(step * (unsigned long long)(long long)pos);
-  // the top 32 bits, in half turns: [-1, 1)
-  const float half = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;      // 2^-31
-  sincospif(half, &s, &c);
+  const unsigned long long phase = step * (unsigned long long)(long long)pos;
+  // the nearest quarter turn, and the rest in half turns: [-1/4, 1/4]
+  const unsigned quarter = (unsigned)((phase + (1ull << 61)) >> 62);
+  const int high = (int)((uint32_t)(phase >> 32) - (quarter << 30));
+  const float rest = fmaf((float)high, 0x1p-31f, (float)(uint32_t)phase * 0x1p-63f);
+  float cr, sr;
+  sincospif(rest, &sr, &cr);
+  c = quarter & 1 ? sr : cr;
+  s = quarter & 1 ? cr : sr;
+  if (quarter == 1 || quarter == 2) c = -c;
+  if (quarter >= 2) s = -s;
   c *= factor;
   s *= inverse ? -factor : factor;
 }
