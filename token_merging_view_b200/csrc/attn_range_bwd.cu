@@ -19,6 +19,13 @@
 //    of three bf16, which holds an fp32 whole (1023 us);
 //  - attn_dq_kernel: a CTA owns 128 queries and walks over their keys; dS is
 //    the A operand of dQ += dS K.
+// Roundings: S, dP, the exponentials and the accumulators are fp32.  P and dS
+// are rounded to bf16, at most 2^-8 of themselves, as operands of the tensor
+// core beside bf16 dO, K and Q.  D comes from out as the forward left it, in
+// bf16: an fp32 copy would be 4 more bytes an element to write and to read;
+// D is off by 2^-8 sum |dout| |out| at most, which dS takes over times P.
+// Over few keys, where P is large, that shows most.
+//
 // Seven products a tile where one fused pass has five: dQ gathered from
 // key-owning CTAs needs either atomics, whose order would change the result
 // from run to run, or N x N / 128 partial sums.

@@ -7,22 +7,26 @@
 // A work item is up to 256 such rows of one key head -- two 128-row tiles,
 // or one when there are no more -- against the union of their key ranges.
 //
-// Long sequences (attn_range_fwd_kernel), 12 warps: warp 0 loads K/V tiles of 128 keys by TMA into a ring of four;
-// warp 1 issues tcgen05.mma (S = Q K^T from shared memory, then O += P V
-// with P read from TMEM); warps 4..7 and 8..11 are the softmax of tiles 0
-// and 1, one row a thread.  TMEM: a ring of three 128-column S buffers (P
+// Long sequences (attn_range_fwd_kernel), 12 warps: warp 0 loads K/V tiles of
+// 128 keys by TMA into a ring of four; warp 1 issues tcgen05.mma (S = Q K^T
+// from shared memory, then O += P V with P read from TMEM); warps 4..7 and
+// 8..11 are the softmax of tiles 0 and 1, one row a thread.  TMEM: a ring of three 128-column S buffers (P
 // overwrites half of its S), O_0 and O_1 of 64 columns: 512.  The i-th S
 // product goes to buffer i % 3 and is issued right behind the P V product
 // that frees it, so the tensor core works on one tile during the other's
 // softmax.  Scores are exponentiated against a maximum in use that is raised
 // (and O rescaled) only when a tile's sum passes 2^16.  Bound by the exp
 // unit together with the cost of the N = 64 MMAs, as the layer's dense
-// attention is; with few rows by the memory that K and V come from.
+// attention is.  (Up to 32 rows a key head have a kernel of their own.)
 //
-// Splits: with fewer items than SMs (single tokens), or a last wave that
-// would run mostly empty, each item's keys are cut in `parts` ranges of
-// whole tiles; the parts leave unnormalised sums and maxima, which
-// attn_join_kernel adds up in order.
+// Splits: with fewer items than SMs, or a last wave that would run mostly
+// empty, each item's keys are cut in `parts` ranges of whole tiles; the parts
+// leave unnormalised sums and maxima, which attn_join_kernel adds up in order.
+//
+// Roundings: scores, the running sum (of the unrounded P) and O are fp32.  P
+// is rounded to bf16, at most 2^-8 of itself, because it is an operand of the
+// tensor core beside a bf16 V: a second product for what the rounding takes
+// off would cost half of the call again.  The result is rounded once.
 //
 // Masks: a tile that every row of a warp sees whole takes no compares.
 // Keys outside the union of the item's ranges never enter: whole tiles are

@@ -4,11 +4,11 @@
 //
 // Bound by the memory K and V come from: a row's arithmetic hides behind its
 // bytes, and a 128-row tensor-core tile would be mostly padding (the tiled
-// kernel took 277 us where this one takes 149, 32 sequences of up to 41,070
+// kernel took 277 us where this one takes 169, 32 sequences of up to 41,070
 // keys).  So every warp works alone: it streams tiles of 32 keys by TMA into
 // a ring of its own (no barrier with another warp until the end), multiplies
 // with the 16-row warp-level MMAs (m16n8k16), and keeps a running maximum,
-// sum and O in registers.  Four warps a block and two blocks an SM keep about
+// sum and O in fp32 registers (P enters P V in bf16, as in the tiled kernels).  Four warps a block and two blocks an SM keep about
 // 128 KB of loads in flight.  At the end the block's warps are added up in
 // order, then the blocks of an item: up to 8 are a cluster and read each
 // other's shared memory (one launch, no workspace); more, for a long cache
