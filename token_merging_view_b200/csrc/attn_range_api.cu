@@ -1,29 +1,12 @@
 // Host side of attention over key ranges: argument checks, tensor maps, the
 // entry points.
 #include <algorithm>
-#include <mutex>
 
 #include "attn_ops.h"
+#include "tensor_map.h"
 
 namespace httm {
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 constexpr int64_t kMaxStride = (int64_t)1 << 38;       // elements: TMA strides stay below 2^40 bytes
 
@@ -98,12 +81,6 @@ bool attn_map(AttnMap* m, const View& v, const void* spare, int d, int tokens, i
 }  // namespace httm
 
 using namespace httm;
-
-#define HTTM_TRY(expr)                   \
-  do {                                   \
-    const httm_status t_ = (expr);       \
-    if (t_ != HTTM_OK) return t_;        \
-  } while (0)
 
 extern "C" {
 

@@ -36,7 +36,6 @@
 // product and added at the end to the rows that see them, so that they reach
 // no other (the check costs such tiles about a tenth, other tiles nothing).
 #include <algorithm>
-#include <mutex>
 
 #include "attn_ops.cuh"
 

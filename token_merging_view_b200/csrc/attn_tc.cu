@@ -41,11 +41,11 @@
 // that runs out sets HTTM_DEV_TIMEOUT, the CTA drains its MMAs, frees TMEM
 // and exits.
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace httm {
 namespace {
@@ -512,23 +512,6 @@ attn_combine_kernel(__nv_bfloat16* __restrict__ O, int Lk, int n_sm, Buffers buf
       }
     }
   }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
 }
 
 // [rows, 64] bf16 row-major, 128-row x 64-column boxes, 128-byte swizzle;

@@ -616,12 +616,6 @@ cudaError_t by_type(const httm_norm_cfg& c, int width, Fn&& fn) {
 
 using namespace httm;
 
-#define HTTM_TRY(expr)                   \
-  do {                                   \
-    const httm_status t_ = (expr);       \
-    if (t_ != HTTM_OK) return t_;        \
-  } while (0)
-
 extern "C" {
 
 httm_status httm_gated_norm_forward(const httm_norm_cfg* c, const httm_norm_weights* w, const httm_rows* x,

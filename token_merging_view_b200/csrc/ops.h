@@ -73,6 +73,12 @@ inline cudaError_t check_registers(int threads, int total) {
   return cudaSuccess;
 }
 
+#define HTTM_TRY(expr)                   \
+  do {                                   \
+    const httm_status t_ = (expr);       \
+    if (t_ != HTTM_OK) return t_;        \
+  } while (0)
+
 #define HTTM_OPS_LAUNCH(expr, s)                              \
   do {                                                        \
     const cudaError_t e_ = ::httm::checked((expr), (s));      \
