@@ -254,3 +254,9 @@ def test_device_status_reads_the_device_that_is_meant(device, index, monkeypatch
     with pytest.raises(Seen) as seen:
         ops.httm_ops_device_status(device)
     assert seen.value.args == (index,)
+
+
+@pytest.mark.parametrize("ns", [-1, 2 ** 64])
+def test_wait_budget_is_within_64_bits(ns):
+    with pytest.raises(ValueError, match="nanoseconds"):
+        ops.httm_ops_set_wait_budget(ns)
